@@ -63,7 +63,8 @@ typedef enum {
   FFDP_ERR_INTERNAL = 5
 } ffdp_status;
 
-typedef enum { FFDP_F32 = 0, FFDP_F16 = 1 } ffdp_dtype;
+/* FFDP_BF16 is taken by the token operators only; volumes are F32 or F16. */
+typedef enum { FFDP_F32 = 0, FFDP_F16 = 1, FFDP_BF16 = 2 } ffdp_dtype;
 
 typedef struct { int64_t d, h, w; } ffdp_dims;
 
@@ -277,6 +278,143 @@ ffdp_status ffdp_sobolev_fwd_bwd(const float *u, ffdp_dims dims, float lambda, f
 ffdp_status ffdp_sobolev_adam_step(const float *u, float *u_out, const float *g, float *m1, float *m2,
                                    ffdp_dims dims, const ffdp_sobolev_adam_params *p, float *loss, void *ws,
                                    size_t ws_bytes, void *stream);
+
+/* ---- token operators ---------------------------------------------------
+ * The displacement u that the objective grades may be the output of a network
+ * over the volumes' patches (a learned registration).  These are the operators
+ * of such a network's blocks over volume tokens: rotary positions with one to
+ * three axes, attention with its masks and biases, and the matrix product
+ * with its epilogue, each with its backward pass.  The network's coarse
+ * displacement grid becomes u through ffdp_sample_channels_fwd, and du goes
+ * back to it through ffdp_sample_channels_bwd.
+ *
+ * Token tensors are [batch][tokens][heads][head_dim] seen through strides (in
+ * elements; the stride of an extent of one is not read), the last axis
+ * contiguous.  Sums, softmax statistics and products accumulate in 32 bits. */
+
+typedef struct {
+  void *ptr;           /* element (b, t, h, c) at ptr[b * sb + t * st + h * sh + c] */
+  int64_t sb, st, sh;
+} ffdp_heads;
+
+/* Rotary positions.  Pair k of the R = sections[0] + .. + sections[axes - 1]
+ * pairs of a head turns by the angle t = pos[token][a(k)] * freq[k], where the
+ * first sections[0] pairs belong to axis 0, the next sections[1] to axis 1, ...:
+ *   (x1, x2) -> (x1 cos t - x2 sin t, x2 cos t + x1 sin t).
+ * Pair k holds channels (2k, 2k + 1) when interleaved, else (k, k + R);
+ * channels from 2R on pass unchanged.  Limits: axes in [1, 3], 1 <= R and
+ * 2 R <= head_dim <= 1024; tensors in [1, 3]; batch * tokens < 2^31. */
+typedef struct {
+  int64_t batch, tokens;
+  int head_dim, axes;
+  int sections[3];
+  int interleaved;
+} ffdp_rope_params;
+
+typedef struct {
+  ffdp_heads x, y;     /* y may be x (in place); otherwise they must not overlap */
+  int heads;
+} ffdp_rope_tensor;
+
+/* Turns `n` tensors (queries and keys, say) of dtype dt (F32, F16 or BF16) in
+ * one launch.  pos: [batch][tokens][axes] float32 with batch stride pos_sb (0:
+ * shared by the batch), finite; freq: [R] float32.  Angles are float32 with the
+ * product's rounding error carried along; no workspace. */
+ffdp_status ffdp_rope_fwd(const ffdp_rope_tensor *t, int n, ffdp_dtype dt, const ffdp_rope_params *p,
+                          const float *pos, int64_t pos_sb, const float *freq, void *stream);
+
+/* The gradient of ffdp_rope_fwd: the same turn by -t (x: dL/dy, y: dL/dx).
+ * Positions and frequencies are constants. */
+ffdp_status ffdp_rope_bwd(const ffdp_rope_tensor *t, int n, ffdp_dtype dt, const ffdp_rope_params *p,
+                          const float *pos, int64_t pos_sb, const float *freq, void *stream);
+
+/* Attention.  For query token i and key token j of a head h (key head
+ * h / (q_heads / k_heads)):
+ *   s_ij = scale q_i.k_j;  s_ij = cap tanh(s_ij / cap) if cap > 0;
+ *   s_ij -= sum_a slopes[h][a] |pos_q[i][a] - pos_k[j][a]|   (if slopes);
+ *   o_i = sum_j softmax_j(s_ij) v_j  over the visible keys j.
+ * Key j is visible to query i if doc_q[i] == doc_k[j] >= 0 (if documents are
+ * given: several volumes packed in one sequence; negative = padding) and, if
+ * causal, j <= i + k_len - q_len or j < prefix[b] (if a prefix is given).
+ * What is masked has no effect, whatever its value (NaN and infinities too).
+ * A query that sees no key gets o = 0, lse = -inf and gives no gradient.
+ * Where a visible key's v (in the backward pass a visible k, q or go) holds a
+ * NaN or an infinity in a tile with masked pairs, the whole result row is NaN.
+ * Limits: head_dim a multiple of 8 in [8, 128]; q_heads a multiple of k_heads;
+ * lengths in [0, 2^24]; F16 or BF16, pointers 16-byte aligned, strides
+ * multiples of 8. */
+typedef struct {
+  int64_t batch, q_len, k_len;
+  int q_heads, k_heads, head_dim;
+  float scale, cap;    /* cap = 0: none */
+  int causal;
+} ffdp_attention_params;
+
+/* Positions, slopes, documents and prefix; every pointer may be NULL (all
+ * DEVICE, constants to the backward pass), slopes and both positions only
+ * together, as doc_q and doc_k.  *_sb: batch strides in elements (0: shared). */
+typedef struct {
+  const float *pos_q, *pos_k;  /* [batch][len][axes], finite */
+  int64_t pos_q_sb, pos_k_sb;
+  const float *slopes;         /* [q_heads][axes], finite */
+  int axes;                    /* 1 to 3 (read only with slopes) */
+  const int32_t *doc_q, *doc_k; /* [batch][len] */
+  int64_t doc_q_sb, doc_k_sb;
+  const int32_t *prefix;       /* [batch]; causal only */
+} ffdp_attention_bias;
+
+/* o: [batch][q_len][q_heads][head_dim]; lse: [batch][q_heads][q_len] float32
+ * (the natural logarithm of the softmax's denominator; needed by the backward
+ * pass) or NULL.  bias may be NULL.  Few query rows over many keys are split
+ * along the keys and joined through the workspace. */
+ffdp_status ffdp_attention_fwd(const ffdp_heads *q, const ffdp_heads *k, const ffdp_heads *v,
+                               const ffdp_heads *o, float *lse, ffdp_dtype dt,
+                               const ffdp_attention_params *p, const ffdp_attention_bias *bias, void *ws,
+                               size_t ws_bytes, void *stream);
+
+/* gq, gk, gv from go = dL/do and the forward pass's o and lse.  The gradients
+ * of a key head are summed over its query heads in a fixed order: results are
+ * the same bits on every run. */
+ffdp_status ffdp_attention_bwd(const ffdp_heads *q, const ffdp_heads *k, const ffdp_heads *v,
+                               const ffdp_heads *o, const float *lse, const ffdp_heads *go,
+                               const ffdp_heads *gq, const ffdp_heads *gk, const ffdp_heads *gv, ffdp_dtype dt,
+                               const ffdp_attention_params *p, const ffdp_attention_bias *bias, void *ws,
+                               size_t ws_bytes, void *stream);
+
+/* Workspace of the forward (backward = 0) or backward (1) pass; 0 for an
+ * invalid request.  Queries the current device's SM count. */
+size_t ffdp_attention_workspace_bytes(const ffdp_attention_params *p, int backward);
+
+/* Matrix product with its epilogue, for x [rows][in], w [out][in]:
+ *   z = x w^T + b;  y = act(z) + r.
+ * Row strides ld* in elements; F16 or BF16, pointers 16-byte aligned and row
+ * strides multiples of 8 (a row may be padded; the padding is not read as
+ * data and not written).  Limits: rows, in, out in [0, 2^30] with in, out >= 1. */
+typedef enum { FFDP_ACT_NONE = 0, FFDP_ACT_RELU = 1, FFDP_ACT_GELU = 2, FFDP_ACT_SILU = 3 } ffdp_act;
+
+typedef struct {
+  int64_t rows, in, out;
+  int act;             /* ffdp_act; GELU is z Phi(z) with the error function */
+} ffdp_linear_params;
+
+/* b: [out] or NULL; r: [rows][out] residual or NULL (may be y); z: [rows][out]
+ * or NULL, the pre-activation rounded to dt, kept for the backward pass of an
+ * activation. */
+ffdp_status ffdp_linear_fwd(const void *x, int64_t ldx, const void *w, int64_t ldw, const void *b, const void *r,
+                            int64_t ldr, void *y, int64_t ldy, void *z, int64_t ldz, ffdp_dtype dt,
+                            const ffdp_linear_params *p, void *ws, size_t ws_bytes, void *stream);
+
+/* With gz = gy act'(z): gx = gz w, gw = gz^T x, gb = sum over rows of gz (the
+ * residual's gradient is gy itself).  z may be NULL without an activation; gx,
+ * gw and gb may each be NULL.  gz is rounded to dt between the products; sums
+ * over rows that are split are joined in a fixed order. */
+ffdp_status ffdp_linear_bwd(const void *x, int64_t ldx, const void *w, int64_t ldw, const void *z, int64_t ldz,
+                            const void *gy, int64_t ldgy, void *gx, int64_t ldgx, void *gw, int64_t ldgw, void *gb,
+                            ffdp_dtype dt, const ffdp_linear_params *p, void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace of ffdp_linear_fwd (backward = 0) or ffdp_linear_bwd (1); 0 may be
+ * a valid answer of the forward pass. */
+size_t ffdp_linear_workspace_bytes(const ffdp_linear_params *p, int backward);
 
 /* Workspace-free variant of ffdp_objective for the MI term (the paper has no
  * counterpart; it exists for callers that cannot allocate device memory).

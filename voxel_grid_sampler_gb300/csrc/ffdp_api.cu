@@ -37,6 +37,15 @@ static ffdp_status cuda_fail(cudaError_t e, const char* where) {
   return fail(FFDP_ERR_CUDA, "%s: %s", where, cudaGetErrorString(e));
 }
 
+void ffdp::clear_error() { g_err[0] = '\0'; }
+
+void ffdp::set_error(const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+}
+
 extern "C" const char* ffdp_last_error(void) { return g_err; }
 
 extern "C" const char* ffdp_status_string(ffdp_status s) {

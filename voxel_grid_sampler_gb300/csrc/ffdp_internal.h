@@ -240,12 +240,18 @@ struct OccCache {
 unsigned take_test_stall();
 // Reads the device error word of the current device (synchronous) and clears it.
 cudaError_t take_device_error(unsigned* v);
+// Device address of that word on the current device, for kernels of other
+// translation units whose waits may give up.
+cudaError_t device_error_word(unsigned** p);
 int sweep1_ctas_per_sm(int mode, int ft, int mt, int bmax);
 int sweep2_ctas_per_sm(int mode, int ft, int mt, int bmax);
 size_t mi_table_bytes(int bmax);
 int lncc_ctas_per_sm(int mode, int ft, int mt, int bmax_or0, int R);
 
-// Timing / launch-count hooks implemented in ffdp_api.cu.
+// Error detail of this host thread (ffdp_last_error), and timing /
+// launch-count hooks, implemented in ffdp_api.cu.
+void clear_error();
+void set_error(const char* fmt, ...);
 void note_launch_begin(const char* name, cudaStream_t s);
 void note_launch_end(cudaStream_t s);
 

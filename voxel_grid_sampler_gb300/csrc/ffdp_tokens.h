@@ -1,0 +1,101 @@
+// ffdp_tokens.h -- argument records and launchers of the token operators
+// (rotary positions, attention, linear), shared by their host ABI
+// (ffdp_tokens_api.cu) and kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ffdp_internal.h"
+
+namespace ffdp {
+
+// Instantiate a body for a dtype code (0 float, 1 half, 2 bfloat16).
+#define FFDP_TOK_SWITCH16(code, T, ...) \
+  do {                                  \
+    if ((code) == 1) {                  \
+      using T = __half;                 \
+      __VA_ARGS__;                      \
+    } else {                            \
+      using T = __nv_bfloat16;          \
+      __VA_ARGS__;                      \
+    }                                   \
+  } while (0)
+
+template <class T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <class T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// [batch][tokens][heads][head_dim] through element strides.
+struct HeadsView {
+  void* p;
+  int64_t sb, st, sh;
+};
+
+struct RopeArgs {
+  HeadsView x[3], y[3];
+  int heads[3];
+  int n;               // tensors
+  int B, S, D, R, axes;
+  int sec[3];
+  const float* pos;    // [B][S][axes], batch stride pos_sb
+  int64_t pos_sb;
+  const float* freq;   // [R]
+  float sign;          // +1 forward, -1 backward
+};
+cudaError_t launch_rope(int dt, int interleaved, int vec, const RopeArgs& a, cudaStream_t s);
+
+struct AttnArgs {
+  HeadsView q, k, v, o, go, gq, gk, gv;
+  float* lse;          // [B][Hq][Sq] or NULL
+  float* delta;        // backward workspace [B][Hq][Sq]
+  int B, Sq, Sk, Hq, Hk, G, D;
+  float scale, cap;
+  int causal;
+  int axes;            // 0: no distance bias
+  const float *pos_q, *pos_k, *slopes;
+  int64_t pos_q_sb, pos_k_sb;
+  const int *doc_q, *doc_k;
+  int64_t doc_q_sb, doc_k_sb;
+  const int* prefix;
+};
+cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attention_bwd(int dt, const AttnArgs& a, cudaStream_t s);
+
+// C[m][n] = sum_k A(m, k) B(n, k), A(m, k) = a[m am + k ak], B likewise.
+struct LinearArgs {
+  const void *a, *b;
+  int64_t am, ak, bn, bk;
+  void* c;             // rows of ldc elements
+  int64_t ldc;
+  int M, N, K;
+  const void* bias;    // [N] or NULL
+  const void* res;     // [M][N] or NULL
+  int64_t ldr;
+  void* z;             // [M][N] or NULL
+  int64_t ldz;
+  int act;
+};
+cudaError_t launch_linear(int dt, const LinearArgs& a, cudaStream_t s);
+
+// gz = gy act'(z) (rounded to the type) and the column sums of gz.
+struct LinearGradArgs {
+  const void *z, *gy;
+  int64_t ldz, ldgy;
+  void* gz;            // or NULL (no activation: gz = gy)
+  int64_t ldgz;
+  float* partial;      // [chunks][N] or NULL
+  void* gb;            // [N] or NULL
+  int M, N, act, chunks;
+};
+int linear_grad_chunks(int M, int N, int sms);
+cudaError_t launch_linear_grad(int dt, const LinearGradArgs& a, cudaStream_t s);
+
+}  // namespace ffdp

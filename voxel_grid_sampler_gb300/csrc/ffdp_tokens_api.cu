@@ -1,0 +1,418 @@
+// ffdp_tokens_api.cu -- C ABI of the token operators (declared in
+// include/ffdp.h): argument validation, workspace layout, launches.
+#include <cmath>
+#include <cstdarg>
+
+#include "../../include/ffdp.h"
+#include "ffdp_tokens.h"
+
+using namespace ffdp;
+
+namespace {
+
+#define FAIL(st, ...)       \
+  do {                      \
+    set_error(__VA_ARGS__); \
+    return st;              \
+  } while (0)
+
+#define TRY(x)                           \
+  do {                                   \
+    const ffdp_status _st = (x);         \
+    if (_st != FFDP_OK) return _st;      \
+  } while (0)
+
+#define LAUNCH(x, where)                                                             \
+  do {                                                                               \
+    const cudaError_t _e = (x);                                                      \
+    if (_e != cudaSuccess) FAIL(FFDP_ERR_CUDA, "%s: %s", where, cudaGetErrorString(_e)); \
+  } while (0)
+
+bool aligned(const void* p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+int sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+  return n > 0 ? n : 1;
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+ffdp_status check_ws(const void* ws, size_t have, size_t need) {
+  if (need && (!ws || have < need)) FAIL(FFDP_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", need, ws ? have : 0);
+  if (need && !aligned(ws, 256)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "workspace must be 256-byte aligned");
+  return FFDP_OK;
+}
+
+ffdp_status check_dt16(ffdp_dtype dt) {
+  if (dt != FFDP_F16 && dt != FFDP_BF16) FAIL(FFDP_ERR_INVALID_ARGUMENT, "dtype must be F16 or BF16");
+  return FFDP_OK;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ rotary
+namespace {
+
+ffdp_status rope(const ffdp_rope_tensor* t, int n, ffdp_dtype dt, const ffdp_rope_params* p, const float* pos,
+                 int64_t pos_sb, const float* freq, float sign, void* stream) {
+  clear_error();
+  if (!t || !p || n < 1 || n > 3) FAIL(FFDP_ERR_INVALID_ARGUMENT, "null tensors or params, or tensors outside [1, 3]");
+  if (dt != FFDP_F32 && dt != FFDP_F16 && dt != FFDP_BF16) FAIL(FFDP_ERR_INVALID_ARGUMENT, "dtype must be F32, F16 or BF16");
+  if (p->axes < 1 || p->axes > 3) FAIL(FFDP_ERR_INVALID_ARGUMENT, "axes must be in [1, 3]");
+  RopeArgs a{};
+  int64_t R = 0;
+  for (int i = 0; i < p->axes; ++i) {
+    if (p->sections[i] < 0) FAIL(FFDP_ERR_INVALID_ARGUMENT, "negative section");
+    a.sec[i] = p->sections[i];
+    R += p->sections[i];
+  }
+  if (p->head_dim < 1 || p->head_dim > 1024 || R < 1 || 2 * R > p->head_dim)
+    FAIL(FFDP_ERR_INVALID_ARGUMENT, "need 1 <= pairs, 2 pairs <= head_dim <= 1024 (got %lld pairs, head_dim %d)", (long long)R,
+         p->head_dim);
+  if (p->batch < 0 || p->tokens < 0 || p->batch > INT32_MAX || p->tokens > INT32_MAX || p->batch * p->tokens > INT32_MAX)
+    FAIL(FFDP_ERR_INVALID_ARGUMENT, "batch * tokens must be in [0, 2^31)");
+  const bool none = p->batch == 0 || p->tokens == 0;
+  const size_t el = dt == FFDP_F32 ? 4 : 2;
+  // widest vector of pairs that divides the pairs and the unrotated tail and
+  // that every pointer and stride is aligned to (16 bytes at most)
+  const int tail = p->head_dim - 2 * (int)R;
+  int vec = dt == FFDP_F32 ? 4 : 8;
+  while (vec > 1 && (R % vec || tail % vec)) vec >>= 1;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].heads < 1 || t[i].heads > 4096) FAIL(FFDP_ERR_INVALID_ARGUMENT, "heads must be in [1, 4096]");
+    if (!none && (!t[i].x.ptr || !t[i].y.ptr)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "null tensor");
+    a.heads[i] = t[i].heads;
+    const ffdp_heads* v[2] = {&t[i].x, &t[i].y};
+    HeadsView* o[2] = {&a.x[i], &a.y[i]};
+    for (int k = 0; k < 2; ++k) {
+      *o[k] = HeadsView{v[k]->ptr, p->batch > 1 ? v[k]->sb : 0, p->tokens > 1 ? v[k]->st : 0,
+                        t[i].heads > 1 ? v[k]->sh : 0};
+      if (!aligned(v[k]->ptr, el)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "tensor not aligned to its elements");
+      while (vec > 1 && (!aligned(v[k]->ptr, vec * el) || o[k]->sb % vec || o[k]->st % vec || o[k]->sh % vec)) vec >>= 1;
+    }
+  }
+  if (none) return FFDP_OK;
+  if (!pos || !freq || !aligned(pos, 4) || !aligned(freq, 4)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "null or misaligned pos or freq");
+  a.n = n;
+  a.B = (int)p->batch;
+  a.S = (int)p->tokens;
+  a.D = p->head_dim;
+  a.R = (int)R;
+  a.axes = p->axes;
+  a.pos = pos;
+  a.pos_sb = pos_sb;
+  a.freq = freq;
+  a.sign = sign;
+  LAUNCH(launch_rope(dt, p->interleaved != 0, vec, a, static_cast<cudaStream_t>(stream)), "rope launch");
+  return FFDP_OK;
+}
+
+}  // namespace
+
+extern "C" ffdp_status ffdp_rope_fwd(const ffdp_rope_tensor* t, int n, ffdp_dtype dt, const ffdp_rope_params* p,
+                                     const float* pos, int64_t pos_sb, const float* freq, void* stream) {
+  return rope(t, n, dt, p, pos, pos_sb, freq, 1.0f, stream);
+}
+
+extern "C" ffdp_status ffdp_rope_bwd(const ffdp_rope_tensor* t, int n, ffdp_dtype dt, const ffdp_rope_params* p,
+                                     const float* pos, int64_t pos_sb, const float* freq, void* stream) {
+  return rope(t, n, dt, p, pos, pos_sb, freq, -1.0f, stream);
+}
+
+// --------------------------------------------------------------- attention
+namespace {
+
+ffdp_status check_attention(const ffdp_attention_params* p) {
+  if (!p) FAIL(FFDP_ERR_INVALID_ARGUMENT, "null params");
+  constexpr int64_t kMaxLen = 1 << 24;
+  if (p->batch < 0 || p->q_len < 0 || p->k_len < 0 || p->q_len > kMaxLen || p->k_len > kMaxLen || p->batch > (1 << 24))
+    FAIL(FFDP_ERR_INVALID_ARGUMENT, "batch and lengths must be in [0, 2^24]");
+  if (p->q_heads < 1 || p->k_heads < 1 || p->q_heads > 4096 || p->q_heads % p->k_heads)
+    FAIL(FFDP_ERR_INVALID_ARGUMENT, "q_heads (at most 4096) must be a multiple of k_heads");
+  if (p->head_dim < 8 || p->head_dim > 128 || p->head_dim % 8)
+    FAIL(FFDP_ERR_INVALID_ARGUMENT, "head_dim must be a multiple of 8 in [8, 128]");
+  if (!std::isfinite(p->scale) || !std::isfinite(p->cap) || p->cap < 0.0f)
+    FAIL(FFDP_ERR_INVALID_ARGUMENT, "scale must be finite, cap finite and >= 0");
+  if (p->batch * ((p->q_len + 127) / 128 + 1) * p->q_heads > INT32_MAX || p->batch * ((p->k_len + 127) / 128 + 1) * p->q_heads > INT32_MAX)
+    FAIL(FFDP_ERR_UNSUPPORTED, "batch * heads * length too large");
+  return FFDP_OK;
+}
+
+ffdp_status heads_view(const ffdp_heads* t, const char* name, int64_t B, int64_t S, int64_t H, int64_t D, bool out,
+                       HeadsView* v) {
+  if (!t) FAIL(FFDP_ERR_INVALID_ARGUMENT, "null %s", name);
+  *v = HeadsView{t->ptr, B > 1 ? t->sb : 0, S > 1 ? t->st : 0, H > 1 ? t->sh : 0};
+  if (B == 0 || S == 0) return FFDP_OK;
+  if (!t->ptr || !aligned(t->ptr, 16)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "%s must be non-null and 16-byte aligned", name);
+  const int64_t e[3] = {B, S, H}, st[3] = {v->sb, v->st, v->sh};
+  for (int i = 0; i < 3; ++i) {
+    if (e[i] <= 1) continue;
+    if (st[i] % 8 || st[i] < D || st[i] >= ((int64_t)1 << 38))
+      FAIL(FFDP_ERR_INVALID_ARGUMENT, "%s strides must be multiples of 8, at least head_dim", name);
+  }
+  (void)out;
+  return FFDP_OK;
+}
+
+ffdp_status fill_attention(const ffdp_attention_params* p, const ffdp_attention_bias* b, AttnArgs& a) {
+  a.B = (int)p->batch;
+  a.Sq = (int)p->q_len;
+  a.Sk = (int)p->k_len;
+  a.Hq = p->q_heads;
+  a.Hk = p->k_heads;
+  a.G = p->q_heads / p->k_heads;
+  a.D = p->head_dim;
+  a.scale = p->scale;
+  a.cap = p->cap;
+  a.causal = p->causal != 0;
+  if (!b) return FFDP_OK;
+  if (b->slopes) {
+    if (b->axes < 1 || b->axes > 3) FAIL(FFDP_ERR_INVALID_ARGUMENT, "axes must be in [1, 3]");
+    if ((!b->pos_q && a.Sq) || (!b->pos_k && a.Sk)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "slopes need both positions");
+    a.axes = b->axes;
+    a.slopes = b->slopes;
+    a.pos_q = b->pos_q;
+    a.pos_k = b->pos_k;
+    a.pos_q_sb = b->pos_q_sb;
+    a.pos_k_sb = b->pos_k_sb;
+  } else if (b->pos_q || b->pos_k) {
+    FAIL(FFDP_ERR_INVALID_ARGUMENT, "positions need slopes");
+  }
+  if (!b->doc_q != !b->doc_k) FAIL(FFDP_ERR_INVALID_ARGUMENT, "doc_q and doc_k only together");
+  a.doc_q = b->doc_q;
+  a.doc_k = b->doc_k;
+  a.doc_q_sb = b->doc_q_sb;
+  a.doc_k_sb = b->doc_k_sb;
+  if (b->prefix && !a.causal) FAIL(FFDP_ERR_INVALID_ARGUMENT, "a prefix needs causal");
+  a.prefix = b->prefix;
+  const void* w[6] = {a.slopes, a.pos_q, a.pos_k, a.doc_q, a.doc_k, a.prefix};
+  for (const void* x : w)
+    if (!aligned(x, 4)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "positions, slopes, documents and prefix must be 4-byte aligned");
+  return FFDP_OK;
+}
+
+size_t attention_ws(const ffdp_attention_params* p, int backward) {
+  if (!backward) return 256;
+  return 256 + round256((size_t)p->batch * p->q_heads * p->q_len * 4);
+}
+
+}  // namespace
+
+extern "C" size_t ffdp_attention_workspace_bytes(const ffdp_attention_params* p, int backward) {
+  clear_error();
+  if (check_attention(p) != FFDP_OK) return 0;
+  return attention_ws(p, backward);
+}
+
+extern "C" ffdp_status ffdp_attention_fwd(const ffdp_heads* q, const ffdp_heads* k, const ffdp_heads* v,
+                                          const ffdp_heads* o, float* lse, ffdp_dtype dt,
+                                          const ffdp_attention_params* p, const ffdp_attention_bias* bias, void* ws,
+                                          size_t ws_bytes, void* stream) {
+  clear_error();
+  TRY(check_attention(p));
+  TRY(check_dt16(dt));
+  AttnArgs a{};
+  TRY(fill_attention(p, bias, a));
+  TRY(heads_view(q, "q", a.B, a.Sq, a.Hq, a.D, false, &a.q));
+  TRY(heads_view(k, "k", a.B, a.Sk, a.Hk, a.D, false, &a.k));
+  TRY(heads_view(v, "v", a.B, a.Sk, a.Hk, a.D, false, &a.v));
+  TRY(heads_view(o, "o", a.B, a.Sq, a.Hq, a.D, true, &a.o));
+  if (!aligned(lse, 4)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "lse must be 4-byte aligned");
+  TRY(check_ws(ws, ws_bytes, attention_ws(p, 0)));
+  a.lse = lse;
+  if (a.B == 0 || a.Sq == 0) return FFDP_OK;
+  LAUNCH(launch_attention_fwd(dt, a, static_cast<cudaStream_t>(stream)), "attention forward launch");
+  return FFDP_OK;
+}
+
+extern "C" ffdp_status ffdp_attention_bwd(const ffdp_heads* q, const ffdp_heads* k, const ffdp_heads* v,
+                                          const ffdp_heads* o, const float* lse, const ffdp_heads* go,
+                                          const ffdp_heads* gq, const ffdp_heads* gk, const ffdp_heads* gv,
+                                          ffdp_dtype dt, const ffdp_attention_params* p,
+                                          const ffdp_attention_bias* bias, void* ws, size_t ws_bytes, void* stream) {
+  clear_error();
+  TRY(check_attention(p));
+  TRY(check_dt16(dt));
+  AttnArgs a{};
+  TRY(fill_attention(p, bias, a));
+  TRY(heads_view(q, "q", a.B, a.Sq, a.Hq, a.D, false, &a.q));
+  TRY(heads_view(k, "k", a.B, a.Sk, a.Hk, a.D, false, &a.k));
+  TRY(heads_view(v, "v", a.B, a.Sk, a.Hk, a.D, false, &a.v));
+  TRY(heads_view(o, "o", a.B, a.Sq, a.Hq, a.D, false, &a.o));
+  TRY(heads_view(go, "go", a.B, a.Sq, a.Hq, a.D, false, &a.go));
+  TRY(heads_view(gq, "gq", a.B, a.Sq, a.Hq, a.D, true, &a.gq));
+  TRY(heads_view(gk, "gk", a.B, a.Sk, a.Hk, a.D, true, &a.gk));
+  TRY(heads_view(gv, "gv", a.B, a.Sk, a.Hk, a.D, true, &a.gv));
+  if (a.B * (int64_t)a.Sq > 0 && (!lse || !aligned(lse, 4))) FAIL(FFDP_ERR_INVALID_ARGUMENT, "lse must be non-null and 4-byte aligned");
+  TRY(check_ws(ws, ws_bytes, attention_ws(p, 1)));
+  a.lse = const_cast<float*>(lse);
+  a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
+  if (a.B == 0) return FFDP_OK;
+  LAUNCH(launch_attention_bwd(dt, a, static_cast<cudaStream_t>(stream)), "attention backward launch");
+  return FFDP_OK;
+}
+
+// ------------------------------------------------------------------ linear
+namespace {
+
+ffdp_status check_linear(const ffdp_linear_params* p) {
+  if (!p) FAIL(FFDP_ERR_INVALID_ARGUMENT, "null params");
+  constexpr int64_t kMax = 1 << 30;
+  if (p->rows < 0 || p->rows > kMax || p->in < 1 || p->in > kMax || p->out < 1 || p->out > kMax)
+    FAIL(FFDP_ERR_INVALID_ARGUMENT, "rows must be in [0, 2^30], in and out in [1, 2^30]");
+  if (p->act < FFDP_ACT_NONE || p->act > FFDP_ACT_SILU) FAIL(FFDP_ERR_INVALID_ARGUMENT, "unknown activation");
+  return FFDP_OK;
+}
+
+ffdp_status check_rows(const void* p, int64_t ld, int64_t cols, int64_t rows, bool optional, const char* name) {
+  if (!p) {
+    if (optional || rows == 0) return FFDP_OK;
+    FAIL(FFDP_ERR_INVALID_ARGUMENT, "null %s", name);
+  }
+  if (!aligned(p, 16)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", name);
+  if (rows > 1 && (ld % 8 || ld < cols || ld >= ((int64_t)1 << 38)))
+    FAIL(FFDP_ERR_INVALID_ARGUMENT, "%s rows must start a multiple of 8 elements apart, at least %lld", name, (long long)cols);
+  return FFDP_OK;
+}
+
+int64_t pad8(int64_t n) { return (n + 7) & ~(int64_t)7; }
+
+// Workspace of the linear passes: gz (with an activation), partial column sums.
+struct LinearWs {
+  size_t gz, partial, total;
+  int chunks;
+};
+LinearWs linear_ws(const ffdp_linear_params* p, int backward) {
+  LinearWs w{};
+  if (!backward) return w;
+  const int n = sms();
+  size_t at = 0;
+  w.gz = at;
+  if (p->act != FFDP_ACT_NONE) at += round256((size_t)p->rows * pad8(p->out) * 2);
+  w.partial = at;
+  w.chunks = linear_grad_chunks((int)p->rows, (int)p->out, n);
+  at += round256((size_t)w.chunks * p->out * 4);
+  w.total = at;
+  return w;
+}
+
+}  // namespace
+
+extern "C" size_t ffdp_linear_workspace_bytes(const ffdp_linear_params* p, int backward) {
+  clear_error();
+  if (check_linear(p) != FFDP_OK) return 0;
+  return linear_ws(p, backward).total;
+}
+
+extern "C" ffdp_status ffdp_linear_fwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* b,
+                                       const void* r, int64_t ldr, void* y, int64_t ldy, void* z, int64_t ldz,
+                                       ffdp_dtype dt, const ffdp_linear_params* p, void* ws, size_t ws_bytes,
+                                       void* stream) {
+  clear_error();
+  TRY(check_linear(p));
+  TRY(check_dt16(dt));
+  TRY(check_rows(x, ldx, p->in, p->rows, false, "x"));
+  TRY(check_rows(w, ldw, p->in, p->out, false, "w"));
+  TRY(check_rows(r, ldr, p->out, p->rows, true, "r"));
+  TRY(check_rows(y, ldy, p->out, p->rows, false, "y"));
+  TRY(check_rows(z, ldz, p->out, p->rows, true, "z"));
+  if (b && !aligned(b, 16)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "b must be 16-byte aligned");
+  const LinearWs l = linear_ws(p, 0);
+  TRY(check_ws(ws, ws_bytes, l.total));
+  if (p->rows == 0) return FFDP_OK;
+  LinearArgs a{};
+  a.a = x;
+  a.am = ldx;
+  a.ak = 1;
+  a.b = w;
+  a.bn = ldw;
+  a.bk = 1;
+  a.c = y;
+  a.ldc = ldy;
+  a.M = (int)p->rows;
+  a.N = (int)p->out;
+  a.K = (int)p->in;
+  a.bias = b;
+  a.res = r;
+  a.ldr = ldr;
+  a.z = z;
+  a.ldz = ldz;
+  a.act = p->act;
+  LAUNCH(launch_linear(dt, a, static_cast<cudaStream_t>(stream)), "linear launch");
+  return FFDP_OK;
+}
+
+extern "C" ffdp_status ffdp_linear_bwd(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* z,
+                                       int64_t ldz, const void* gy, int64_t ldgy, void* gx, int64_t ldgx, void* gw,
+                                       int64_t ldgw, void* gb, ffdp_dtype dt, const ffdp_linear_params* p, void* ws,
+                                       size_t ws_bytes, void* stream) {
+  clear_error();
+  TRY(check_linear(p));
+  TRY(check_dt16(dt));
+  TRY(check_rows(x, ldx, p->in, p->rows, !gw, "x"));
+  TRY(check_rows(w, ldw, p->in, p->out, !gx, "w"));
+  TRY(check_rows(z, ldz, p->out, p->rows, p->act == FFDP_ACT_NONE, "z"));
+  TRY(check_rows(gy, ldgy, p->out, p->rows, false, "gy"));
+  TRY(check_rows(gx, ldgx, p->in, p->rows, true, "gx"));
+  TRY(check_rows(gw, ldgw, p->in, p->out, true, "gw"));
+  if (gb && !aligned(gb, 16)) FAIL(FFDP_ERR_INVALID_ARGUMENT, "gb must be 16-byte aligned");
+  const LinearWs l = linear_ws(p, 1);
+  TRY(check_ws(ws, ws_bytes, l.total));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool act = p->act != FFDP_ACT_NONE;
+  const void* gz = gy;
+  int64_t ldgz = ldgy;
+  if (gb || act) {
+    LinearGradArgs g{};
+    g.z = z;
+    g.ldz = ldz;
+    g.gy = gy;
+    g.ldgy = ldgy;
+    if (act) {
+      g.gz = static_cast<char*>(ws) + l.gz;
+      g.ldgz = pad8(p->out);
+      gz = g.gz;
+      ldgz = g.ldgz;
+    }
+    g.gb = gb;
+    if (gb) g.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + l.partial);
+    g.M = (int)p->rows;
+    g.N = (int)p->out;
+    g.act = p->act;
+    g.chunks = l.chunks;
+    LAUNCH(launch_linear_grad(dt, g, s), "linear gradient launch");
+  }
+  if (gx && p->rows) {
+    LinearArgs a{};
+    a.a = gz;
+    a.am = ldgz;
+    a.ak = 1;
+    a.b = w;
+    a.bn = 1;
+    a.bk = ldw;
+    a.c = gx;
+    a.ldc = ldgx;
+    a.M = (int)p->rows;
+    a.N = (int)p->in;
+    a.K = (int)p->out;
+    LAUNCH(launch_linear(dt, a, s), "linear gx launch");
+  }
+  if (gw) {
+    LinearArgs a{};
+    a.a = gz;
+    a.am = 1;
+    a.ak = ldgz;
+    a.b = x;
+    a.bn = 1;
+    a.bk = ldx;
+    a.c = gw;
+    a.ldc = ldgw;
+    a.M = (int)p->out;
+    a.N = (int)p->in;
+    a.K = (int)p->rows;
+    LAUNCH(launch_linear(dt, a, s), "linear gw launch");
+  }
+  return FFDP_OK;
+}

@@ -1,0 +1,141 @@
+// k_rope.cu -- rotary positions with one to three axes.
+//
+// Pair k of a head turns by t = pos[token][axis(k)] * freq[k]; the angle is the
+// same for every head of every tensor of a token, so a CTA computes the sines
+// and cosines of its tokens once into shared memory and then streams the heads.
+// Bound by HBM: each element is read and written once.
+#include "ffdp_tokens.h"
+
+namespace ffdp {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+// VEC elements of T as one aligned load / store (VEC * sizeof(T) <= 16 bytes).
+template <class T, int VEC>
+struct alignas(VEC * sizeof(T)) Vec {
+  T e[VEC];
+};
+
+template <class T, int VEC>
+__device__ __forceinline__ void load(const T* p, float* f) {
+  const Vec<T, VEC> v = *reinterpret_cast<const Vec<T, VEC>*>(p);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) f[i] = to_f32<T>(v.e[i]);
+}
+
+template <class T, int VEC>
+__device__ __forceinline__ void store(T* p, const float* f) {
+  Vec<T, VEC> v;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) v.e[i] = from_f32<T>(f[i]);
+  *reinterpret_cast<Vec<T, VEC>*>(p) = v;
+}
+
+// A unit is VEC pairs of one head of one token, or VEC channels of the
+// unrotated tail.  Units of a token: first every head's pair units, then every
+// head's tail units.  A thread keeps its unit and walks the CTA's tokens.
+template <class T, int VEC, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs a, int tokens_per_cta) {
+  extern __shared__ float2 cs[];  // [tokens_per_cta][R]
+  const int total = a.B * a.S;
+  const int t0 = blockIdx.x * tokens_per_cta;
+  const int nt = min(tokens_per_cta, total - t0);
+  for (int i = threadIdx.x; i < nt * a.R; i += kRopeThreads) {
+    const int t = i / a.R, k = i - t * a.R;
+    const int b = (t0 + t) / a.S, s = (t0 + t) - b * a.S;
+    const int ax = k < a.sec[0] ? 0 : (k < a.sec[0] + a.sec[1] ? 1 : 2);
+    const float x = a.pos[b * a.pos_sb + (int64_t)s * a.axes + ax], f = a.freq[k];
+    // the product's rounding error e moves sin and cos by e cos and -e sin
+    const float t1 = x * f, e = fmaf(x, f, -t1);
+    float sn, cn;
+    sincosf(t1, &sn, &cn);
+    cs[i] = make_float2(fmaf(-e, sn, cn), a.sign * fmaf(e, cn, sn));
+  }
+  __syncthreads();
+  const int pu = a.R / VEC, tu = (a.D - 2 * a.R) / VEC, per_head = pu + tu;
+  const int heads = a.heads[0] + (a.n > 1 ? a.heads[1] : 0) + (a.n > 2 ? a.heads[2] : 0);
+  const int units = heads * per_head;
+  const int lanes = units < kRopeThreads ? kRopeThreads / units : 1;  // tokens in flight per CTA
+  const int tl = units < kRopeThreads ? threadIdx.x / units : 0;
+  if (tl >= lanes) return;
+  for (int u = units < kRopeThreads ? threadIdx.x - tl * units : threadIdx.x; u < units; u += kRopeThreads) {
+    int h = u / per_head;
+    const int c = u - h * per_head;
+    int w = 0;
+    while (h >= a.heads[w]) h -= a.heads[w++];
+    const bool tail = c >= pu;
+    if (tail && a.x[w].p == a.y[w].p) continue;
+    const int64_t off_x = (int64_t)h * a.x[w].sh, off_y = (int64_t)h * a.y[w].sh;
+    const T* xp = static_cast<const T*>(a.x[w].p) + off_x;
+    T* yp = static_cast<T*>(a.y[w].p) + off_y;
+    const int k0 = c * VEC;
+    for (int t = tl; t < nt; t += lanes) {
+      const int b = (t0 + t) / a.S, s = (t0 + t) - b * a.S;
+      const T* x = xp + b * a.x[w].sb + (int64_t)s * a.x[w].st;
+      T* y = yp + b * a.y[w].sb + (int64_t)s * a.y[w].st;
+      if (tail) {
+        const int at = 2 * a.R + (c - pu) * VEC;
+        *reinterpret_cast<Vec<T, VEC>*>(y + at) = *reinterpret_cast<const Vec<T, VEC>*>(x + at);
+        continue;
+      }
+      const float2* r = cs + t * a.R + k0;
+      float f[2 * VEC], g[2 * VEC];
+      const int lo = INTER ? 2 * k0 : k0, hi = INTER ? 2 * k0 + VEC : k0 + a.R;
+      load<T, VEC>(x + lo, f);
+      load<T, VEC>(x + hi, f + VEC);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float2 v = r[i];
+        const int p = INTER ? 2 * i : i, q = INTER ? 2 * i + 1 : i + VEC;
+        g[p] = fmaf(f[p], v.x, -f[q] * v.y);
+        g[q] = fmaf(f[q], v.x, f[p] * v.y);
+      }
+      store<T, VEC>(y + lo, g);
+      store<T, VEC>(y + hi, g + VEC);
+    }
+  }
+}
+
+template <class T, int VEC>
+cudaError_t run(bool inter, const RopeArgs& a, cudaStream_t s) {
+  // 8 tokens per CTA: about one sine and cosine per thread at 32 pairs, and
+  // several independent 16-byte loads per thread in flight; fewer where the
+  // table would pass 32 KB
+  int tokens = 8;
+  while (tokens > 1 && tokens * a.R * (int)sizeof(float2) > 32768) tokens >>= 1;
+  const int grid = (a.B * a.S + tokens - 1) / tokens;
+  const size_t smem = (size_t)tokens * a.R * sizeof(float2);
+  note_launch_begin("k_rope", s);
+  if (inter)
+    k_rope<T, VEC, true><<<grid, kRopeThreads, smem, s>>>(a, tokens);
+  else
+    k_rope<T, VEC, false><<<grid, kRopeThreads, smem, s>>>(a, tokens);
+  note_launch_end(s);
+  return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t run16(bool inter, int vec, const RopeArgs& a, cudaStream_t s) {
+  switch (vec) {
+    case 8: return run<T, 8>(inter, a, s);
+    case 4: return run<T, 4>(inter, a, s);
+    case 2: return run<T, 2>(inter, a, s);
+    default: return run<T, 1>(inter, a, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(int dt, int interleaved, int vec, const RopeArgs& a, cudaStream_t s) {
+  if (dt == 1) return run16<__half>(interleaved, vec, a, s);
+  if (dt == 2) return run16<__nv_bfloat16>(interleaved, vec, a, s);
+  switch (vec) {
+    case 4: return run<float, 4>(interleaved, a, s);
+    case 2: return run<float, 2>(interleaved, a, s);
+    default: return run<float, 1>(interleaved, a, s);
+  }
+}
+
+}  // namespace ffdp

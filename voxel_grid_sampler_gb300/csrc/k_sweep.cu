@@ -1186,6 +1186,13 @@ cudaError_t take_device_error(unsigned* v) {
   return e;
 }
 
+cudaError_t device_error_word(unsigned** p) {
+  void* a = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&a, g_ffdp_device_error);
+  *p = static_cast<unsigned*>(a);
+  return e;
+}
+
 size_t mi_table_bytes(int bmax) { return (size_t)(bmax == 32 ? table_floats<32>() : table_floats<64>()) * sizeof(float); }
 
 }  // namespace ffdp

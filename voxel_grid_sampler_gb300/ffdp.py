@@ -18,10 +18,11 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libffdp.so")
 
-FFDP_F32, FFDP_F16 = 0, 1
+FFDP_F32, FFDP_F16, FFDP_BF16 = 0, 1, 2
 FFDP_OP_GRID_SAMPLE_BWD, FFDP_OP_MI, FFDP_OP_LNCC, FFDP_OP_OBJECTIVE = 1, 2, 3, 4
 FFDP_OP_SAMPLE_CHANNELS_BWD, FFDP_OP_MSE, FFDP_OP_OBJECTIVE_MSE, FFDP_OP_SOBOLEV = 5, 6, 7, 8
 FFDP_OP_OBJECTIVE_STORED = 9
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 STATUS = {0: "FFDP_OK", 1: "FFDP_ERR_INVALID_ARGUMENT", 2: "FFDP_ERR_UNSUPPORTED",
           3: "FFDP_ERR_WORKSPACE", 4: "FFDP_ERR_CUDA", 5: "FFDP_ERR_INTERNAL"}
 
@@ -58,6 +59,36 @@ class ffdp_sobolev_adam_params(ctypes.Structure):
 class ffdp_objective_params(ctypes.Structure):
     _fields_ = [("w_mi", ctypes.c_float), ("w_lncc", ctypes.c_float), ("mi", ffdp_mi_params),
                 ("lncc", ffdp_lncc_params)]
+
+
+class ffdp_heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("sb", ctypes.c_int64), ("st", ctypes.c_int64), ("sh", ctypes.c_int64)]
+
+
+class ffdp_rope_params(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("tokens", ctypes.c_int64), ("head_dim", ctypes.c_int),
+                ("axes", ctypes.c_int), ("sections", ctypes.c_int * 3), ("interleaved", ctypes.c_int)]
+
+
+class ffdp_rope_tensor(ctypes.Structure):
+    _fields_ = [("x", ffdp_heads), ("y", ffdp_heads), ("heads", ctypes.c_int)]
+
+
+class ffdp_attention_params(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("q_len", ctypes.c_int64), ("k_len", ctypes.c_int64),
+                ("q_heads", ctypes.c_int), ("k_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("scale", ctypes.c_float), ("cap", ctypes.c_float), ("causal", ctypes.c_int)]
+
+
+class ffdp_attention_bias(ctypes.Structure):
+    _fields_ = [("pos_q", ctypes.c_void_p), ("pos_k", ctypes.c_void_p), ("pos_q_sb", ctypes.c_int64),
+                ("pos_k_sb", ctypes.c_int64), ("slopes", ctypes.c_void_p), ("axes", ctypes.c_int),
+                ("doc_q", ctypes.c_void_p), ("doc_k", ctypes.c_void_p), ("doc_q_sb", ctypes.c_int64),
+                ("doc_k_sb", ctypes.c_int64), ("prefix", ctypes.c_void_p)]
+
+
+class ffdp_linear_params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("in_", ctypes.c_int64), ("out", ctypes.c_int64), ("act", ctypes.c_int)]
 
 
 _lib = None
@@ -102,7 +133,24 @@ def lib() -> ctypes.CDLL:
         L.ffdp_sobolev_adam_step.argtypes = [_vp, _vp, _vp, _vp, _vp, ffdp_dims,
                                              ctypes.POINTER(ffdp_sobolev_adam_params), _vp, _vp, ctypes.c_size_t,
                                              _vp]
-        for f in ("ffdp_grid_sample_fwd", "ffdp_grid_sample_bwd", "ffdp_mi_fwd_bwd",
+        i64, sz, hp = ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(ffdp_heads)
+        for f in ("ffdp_rope_fwd", "ffdp_rope_bwd"):
+            getattr(L, f).argtypes = [ctypes.POINTER(ffdp_rope_tensor), ctypes.c_int, ctypes.c_int,
+                                      ctypes.POINTER(ffdp_rope_params), _vp, i64, _vp, _vp]
+        ap, bp = ctypes.POINTER(ffdp_attention_params), ctypes.POINTER(ffdp_attention_bias)
+        L.ffdp_attention_fwd.argtypes = [hp] * 4 + [_vp, ctypes.c_int, ap, bp, _vp, sz, _vp]
+        L.ffdp_attention_bwd.argtypes = [hp] * 4 + [_vp] + [hp] * 4 + [ctypes.c_int, ap, bp, _vp, sz, _vp]
+        L.ffdp_attention_workspace_bytes.argtypes = [ap, ctypes.c_int]
+        L.ffdp_attention_workspace_bytes.restype = sz
+        lp = ctypes.POINTER(ffdp_linear_params)
+        L.ffdp_linear_fwd.argtypes = [_vp, i64, _vp, i64, _vp, _vp, i64, _vp, i64, _vp, i64, ctypes.c_int, lp, _vp, sz,
+                                      _vp]
+        L.ffdp_linear_bwd.argtypes = [_vp, i64, _vp, i64, _vp, i64, _vp, i64, _vp, i64, _vp, i64, _vp, ctypes.c_int, lp,
+                                      _vp, sz, _vp]
+        L.ffdp_linear_workspace_bytes.argtypes = [lp, ctypes.c_int]
+        L.ffdp_linear_workspace_bytes.restype = sz
+        for f in ("ffdp_rope_fwd", "ffdp_rope_bwd", "ffdp_attention_fwd", "ffdp_attention_bwd", "ffdp_linear_fwd",
+                  "ffdp_linear_bwd", "ffdp_grid_sample_fwd", "ffdp_grid_sample_bwd", "ffdp_mi_fwd_bwd",
                   "ffdp_lncc_fwd_bwd", "ffdp_objective", "ffdp_objective_stored", "ffdp_sample_channels_fwd",
                   "ffdp_sample_channels_bwd", "ffdp_mse_fwd_bwd", "ffdp_objective_mse",
                   "ffdp_sobolev_fwd_bwd", "ffdp_sobolev_adam_step"):
@@ -408,6 +456,248 @@ def ffdp_sobolev_adam_step(u, g, m1, m2, params: ffdp_sobolev_adam_params, u_out
     _check(lib().ffdp_sobolev_adam_step(_ptr(u), _ptr(u_out), _ptr(g), _ptr(m1), _ptr(m2), dims_of(shape),
                                         ctypes.byref(params), _ptr(loss), _ptr(ws), ws.numel(), _stream(stream)))
     return u_out, loss
+
+
+# ----------------------------------------------------------- token operators
+# Token tensors are (batch, tokens, heads, head_dim) with any strides the
+# library takes (last axis contiguous); matrices are (rows, columns) with
+# contiguous rows that may be padded.  Outputs default to contiguous tensors
+# (matrices: rows padded to 16 bytes).
+_DTYPES = {torch.float32: FFDP_F32, torch.float16: FFDP_F16, torch.bfloat16: FFDP_BF16}
+
+
+def _tok(t, name, like=None, shape=None):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise FfdpError(1, "%s must be a CUDA tensor" % name)
+    if t.dtype not in _DTYPES:
+        raise FfdpError(1, "%s must be float32, float16 or bfloat16, got %s" % (name, t.dtype))
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise FfdpError(1, "%s must have the type and device of the first tensor" % name)
+    if shape is not None and t.shape != shape:
+        raise FfdpError(1, "%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dim() > 1 and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise FfdpError(1, "%s must have a contiguous last axis" % name)
+    return t
+
+
+def _heads(t) -> ffdp_heads:
+    s = t.stride()
+    return ffdp_heads(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _const(t, name, dtype, device, tail):
+    """A constant array of shape tail, or (batch,) + tail: its pointer and batch stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device or t.dtype != dtype:
+        raise FfdpError(1, "%s must be a %s CUDA tensor on the tensors' device" % (name, dtype))
+    if t.shape[-len(tail):] != tail or t.dim() not in (len(tail), len(tail) + 1):
+        raise FfdpError(1, "%s must have shape %s, with or without a batch axis, got %s" % (name, tail, tuple(t.shape)))
+    inner = t[0] if t.dim() > len(tail) and t.shape[0] else t
+    if not inner.is_contiguous():
+        raise FfdpError(1, "%s must be contiguous within the batch" % name)
+    return t.data_ptr(), t.stride(0) if t.dim() > len(tail) and t.shape[0] > 1 else 0
+
+
+def _batch_of(t, tail_dims, B, name):
+    if t.dim() > tail_dims and t.shape[0] != B:
+        raise FfdpError(1, "%s has a batch of %d, the tensors %d" % (name, t.shape[0], B))
+
+
+def _rope(fn, x, pos, freq, sections, interleaved, x2, y, y2, stream):
+    _tok(x, "x")
+    if x.dim() != 4:
+        raise FfdpError(1, "x must be (batch, tokens, heads, head_dim)")
+    B, S, _, D = x.shape
+    if not 1 <= len(sections) <= 3:
+        raise FfdpError(1, "sections must name one to three axes")
+    pp, psb = _const(pos, "pos", torch.float32, x.device, (S, len(sections)))
+    _batch_of(pos, 2, B, "pos")
+    fp, _ = _const(freq, "freq", torch.float32, x.device, (sum(sections),))
+    if freq.dim() != 1:
+        raise FfdpError(1, "freq must have one axis")
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else _tok(y, "y", x, x.shape)
+    t = (ffdp_rope_tensor * 2)()
+    t[0] = ffdp_rope_tensor(_heads(x), _heads(y), x.shape[2])
+    if x2 is not None:
+        _tok(x2, "x2", x)
+        if x2.dim() != 4 or x2.shape[:2] != x.shape[:2] or x2.shape[3] != D:
+            raise FfdpError(1, "x2 must have x's batch, tokens and head_dim")
+        y2 = torch.empty(x2.shape, dtype=x.dtype, device=x.device) if y2 is None else _tok(y2, "y2", x, x2.shape)
+        t[1] = ffdp_rope_tensor(_heads(x2), _heads(y2), x2.shape[2])
+    p = ffdp_rope_params(B, S, D, len(sections), (ctypes.c_int * 3)(*sections), int(bool(interleaved)))
+    _check(fn(t, 1 if x2 is None else 2, _DTYPES[x.dtype], ctypes.byref(p), pp, psb, fp, _stream(stream)))
+    return y if x2 is None else (y, y2)
+
+
+def ffdp_rope_fwd(x, pos, freq, sections, interleaved=False, x2=None, y=None, y2=None, stream=None):
+    """Rotary positions: turns x (and x2, e.g. queries and keys) by pos[..., axis] * freq.
+
+    pos: (tokens, axes) or (batch, tokens, axes); freq: (sum(sections),);
+    sections: pairs per axis.  Returns y, or (y, y2) with x2; y may be x."""
+    return _rope(lib().ffdp_rope_fwd, x, pos, freq, sections, interleaved, x2, y, y2, stream)
+
+
+def ffdp_rope_bwd(gy, pos, freq, sections, interleaved=False, gy2=None, gx=None, gx2=None, stream=None):
+    """Gradient of ffdp_rope_fwd with respect to its tensors."""
+    return _rope(lib().ffdp_rope_bwd, gy, pos, freq, sections, interleaved, gy2, gx, gx2, stream)
+
+
+def attention_params(scale, cap=0.0, causal=False) -> ffdp_attention_params:
+    """scale, cap (0: none) and causality; the calls fill in the shapes."""
+    return ffdp_attention_params(0, 0, 0, 1, 1, 8, float(scale), float(cap), int(bool(causal)))
+
+
+def _attention_shapes(q, k, v, params):
+    _tok(q, "q")
+    _tok(k, "k", q)
+    _tok(v, "v", q, k.shape)
+    if q.dim() != 4 or k.dim() != 4 or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3]:
+        raise FfdpError(1, "q and k must be (batch, tokens, heads, head_dim) with one batch and head_dim")
+    return ffdp_attention_params(q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3], params.scale,
+                                 params.cap, params.causal)
+
+
+def _attention_bias(q, k, pos_q, pos_k, slopes, doc_q, doc_k, prefix):
+    if pos_q is None and pos_k is None and slopes is None and doc_q is None and doc_k is None and prefix is None:
+        return None
+    b, dev, B = ffdp_attention_bias(), q.device, q.shape[0]
+    if slopes is not None:
+        if slopes.dim() != 2 or slopes.shape[0] != q.shape[2] or not 1 <= slopes.shape[1] <= 3:
+            raise FfdpError(1, "slopes must be (q_heads, axes) with one to three axes")
+        b.axes = slopes.shape[1]
+        b.slopes, _ = _const(slopes, "slopes", torch.float32, dev, tuple(slopes.shape))
+    axes = b.axes or 1
+    if pos_q is not None:
+        b.pos_q, b.pos_q_sb = _const(pos_q, "pos_q", torch.float32, dev, (q.shape[1], axes))
+        _batch_of(pos_q, 2, B, "pos_q")
+    if pos_k is not None:
+        b.pos_k, b.pos_k_sb = _const(pos_k, "pos_k", torch.float32, dev, (k.shape[1], axes))
+        _batch_of(pos_k, 2, B, "pos_k")
+    if doc_q is not None:
+        b.doc_q, b.doc_q_sb = _const(doc_q, "doc_q", torch.int32, dev, (q.shape[1],))
+        _batch_of(doc_q, 1, B, "doc_q")
+    if doc_k is not None:
+        b.doc_k, b.doc_k_sb = _const(doc_k, "doc_k", torch.int32, dev, (k.shape[1],))
+        _batch_of(doc_k, 1, B, "doc_k")
+    if prefix is not None:
+        b.prefix, _ = _const(prefix, "prefix", torch.int32, dev, (B,))
+    return ctypes.byref(b)
+
+
+def _attention_ws(p, backward, ws, device):
+    if ws is None:
+        n = int(lib().ffdp_attention_workspace_bytes(ctypes.byref(p), backward))
+        if n == 0:
+            raise FfdpError(1, (lib().ffdp_last_error() or b"").decode())
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+    return ws
+
+
+def ffdp_attention_fwd(q, k, v, params: ffdp_attention_params, pos_q=None, pos_k=None, slopes=None, doc_q=None,
+                       doc_k=None, prefix=None, o=None, lse=None, ws=None, stream=None, want_lse=True):
+    """Attention of q (B, Sq, Hq, D) over k, v (B, Sk, Hk, D): returns (o, lse); lse (B, Hq, Sq) float32 is
+    what the backward pass needs (None unless asked for).
+
+    slopes (Hq, axes) with pos_q, pos_k ([B,] S, axes) float32: distance bias; doc_q, doc_k ([B,] S) int32:
+    documents (negative: padding); prefix (B,) int32: keys visible to every query of a causal call."""
+    p = _attention_shapes(q, k, v, params)
+    bias = _attention_bias(q, k, pos_q, pos_k, slopes, doc_q, doc_k, prefix)
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else _tok(o, "o", q, q.shape)
+    if lse is None and want_lse:
+        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
+    elif lse is not None:
+        _dev(lse, "lse", torch.float32, 3)
+    ws = _attention_ws(p, 0, ws, q.device)
+    _check(lib().ffdp_attention_fwd(_heads(q), _heads(k), _heads(v), _heads(o), _ptr(lse), _DTYPES[q.dtype],
+                                    ctypes.byref(p), bias, _ptr(ws), ws.numel(), _stream(stream)))
+    return o, lse
+
+
+def ffdp_attention_bwd(q, k, v, o, lse, go, params: ffdp_attention_params, pos_q=None, pos_k=None, slopes=None,
+                       doc_q=None, doc_k=None, prefix=None, gq=None, gk=None, gv=None, ws=None, stream=None):
+    """Gradients (gq, gk, gv) of ffdp_attention_fwd from its o and lse and go = dL/do."""
+    p = _attention_shapes(q, k, v, params)
+    bias = _attention_bias(q, k, pos_q, pos_k, slopes, doc_q, doc_k, prefix)
+    _tok(o, "o", q, q.shape)
+    _tok(go, "go", q, q.shape)
+    _dev(lse, "lse", torch.float32, 3)
+    if tuple(lse.shape) != (q.shape[0], q.shape[2], q.shape[1]):
+        raise FfdpError(1, "lse must be (batch, q_heads, q_len)")
+    gq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if gq is None else _tok(gq, "gq", q, q.shape)
+    gk = torch.empty(k.shape, dtype=q.dtype, device=q.device) if gk is None else _tok(gk, "gk", q, k.shape)
+    gv = torch.empty(k.shape, dtype=q.dtype, device=q.device) if gv is None else _tok(gv, "gv", q, k.shape)
+    ws = _attention_ws(p, 1, ws, q.device)
+    _check(lib().ffdp_attention_bwd(_heads(q), _heads(k), _heads(v), _heads(o), _ptr(lse), _heads(go), _heads(gq),
+                                    _heads(gk), _heads(gv), _DTYPES[q.dtype], ctypes.byref(p), bias, _ptr(ws),
+                                    ws.numel(), _stream(stream)))
+    return gq, gk, gv
+
+
+def _matrix(rows, cols, like):
+    """Uninitialised (rows, cols) whose rows start on 16 bytes."""
+    return torch.empty((rows, -(-cols // 8) * 8), dtype=like.dtype, device=like.device)[:, :cols]
+
+
+def _ld(t):
+    return 0 if t is None else t.stride(0)
+
+
+def _linear_shapes(x, w, act):
+    _tok(x, "x")
+    _tok(w, "w", x)
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise FfdpError(1, "x must be (rows, in) and w (out, in)")
+    if act not in ACTS:
+        raise FfdpError(1, "act must be one of %s" % sorted(ACTS))
+    return ffdp_linear_params(x.shape[0], x.shape[1], w.shape[0], ACTS[act])
+
+
+def _linear_ws(p, backward, ws, device):
+    if ws is None:
+        n = int(lib().ffdp_linear_workspace_bytes(ctypes.byref(p), backward))
+        ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    return ws
+
+
+def ffdp_linear_fwd(x, w, b=None, r=None, act="none", y=None, z=None, ws=None, stream=None, want_z=False):
+    """y = act(x w^T + b) + r for x (rows, in), w (out, in): returns (y, z); z, the pre-activation that the
+    backward pass of an activation needs, is None unless asked for (or without an activation)."""
+    p = _linear_shapes(x, w, act)
+    M, N = x.shape[0], w.shape[0]
+    if b is not None and _tok(b, "b", x, (N,)).stride(0) != 1 and N > 1:
+        raise FfdpError(1, "b must be contiguous")
+    if r is not None:
+        _tok(r, "r", x, (M, N))
+    y = _matrix(M, N, x) if y is None else _tok(y, "y", x, (M, N))
+    if z is None and want_z and act != "none":
+        z = _matrix(M, N, x)
+    elif z is not None:
+        _tok(z, "z", x, (M, N))
+    ws = _linear_ws(p, 0, ws, x.device)
+    _check(lib().ffdp_linear_fwd(_ptr(x), _ld(x), _ptr(w), _ld(w), _ptr(b), _ptr(r), _ld(r), _ptr(y), _ld(y), _ptr(z),
+                                 _ld(z), _DTYPES[x.dtype], ctypes.byref(p), _ptr(ws), 0 if ws is None else ws.numel(),
+                                 _stream(stream)))
+    return y, z
+
+
+def ffdp_linear_bwd(x, w, z, gy, act="none", gx=None, gw=None, gb=None, ws=None, stream=None, want_gx=True,
+                    want_gw=True, want_gb=True):
+    """Gradients (gx, gw, gb) of ffdp_linear_fwd from gy = dL/dy (None where not wanted)."""
+    p = _linear_shapes(x, w, act)
+    M, K, N = x.shape[0], x.shape[1], w.shape[0]
+    _tok(gy, "gy", x, (M, N))
+    if z is not None:
+        _tok(z, "z", x, (M, N))
+    gx = _matrix(M, K, x) if gx is None and want_gx else gx
+    gw = _matrix(N, K, x) if gw is None and want_gw else gw
+    gb = torch.empty(N, dtype=x.dtype, device=x.device) if gb is None and want_gb else gb
+    for t, n, shape in ((gx, "gx", (M, K)), (gw, "gw", (N, K)), (gb, "gb", (N,))):
+        if t is not None:
+            _tok(t, n, x, shape)
+    ws = _linear_ws(p, 1, ws, x.device)
+    _check(lib().ffdp_linear_bwd(_ptr(x), _ld(x), _ptr(w), _ld(w), _ptr(z), _ld(z), _ptr(gy), _ld(gy), _ptr(gx), _ld(gx),
+                                 _ptr(gw), _ld(gw), _ptr(gb), _DTYPES[x.dtype], ctypes.byref(p), _ptr(ws),
+                                 0 if ws is None else ws.numel(), _stream(stream)))
+    return gx, gw, gb
 
 
 def launch_count() -> int:
