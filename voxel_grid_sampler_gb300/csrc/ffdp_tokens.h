@@ -69,10 +69,12 @@ struct AttnArgs {
 cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attention_bwd(int dt, const AttnArgs& a, cudaStream_t s);
 
-// C[m][n] = sum_k A(m, k) B(n, k), A(m, k) = a[m am + k ak], B likewise.
+// C[m][n] = sum_k A(m, k) B(n, k).  An operand is K-major (rows m or n of K
+// elements) or MN-major (rows k of M or N elements), rows ld elements apart.
 struct LinearArgs {
   const void *a, *b;
-  int64_t am, ak, bn, bk;
+  int a_mn, b_mn;
+  int64_t lda, ldb;
   void* c;             // rows of ldc elements
   int64_t ldc;
   int M, N, K;
@@ -83,7 +85,12 @@ struct LinearArgs {
   int64_t ldz;
   int act;
 };
-cudaError_t launch_linear(int dt, const LinearArgs& a, cudaStream_t s);
+struct LinearPlan {
+  int bn, splits;
+  size_t partial_bytes;
+};
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int sms);
+cudaError_t launch_linear(int dt, const LinearArgs& a, int sms, float* partial, cudaStream_t s);
 
 // gz = gy act'(z) (rounded to the type) and the column sums of gz.
 struct LinearGradArgs {

@@ -279,22 +279,31 @@ ffdp_status check_rows(const void* p, int64_t ld, int64_t cols, int64_t rows, bo
 
 int64_t pad8(int64_t n) { return (n + 7) & ~(int64_t)7; }
 
-// Workspace of the linear passes: gz (with an activation), partial column sums.
+// Workspace of the linear passes: gz (with an activation), partial column
+// sums, and one area for the partial products of the calls' products, which
+// run one after the other.
 struct LinearWs {
-  size_t gz, partial, total;
-  int chunks;
+  size_t gz, partial, product, total;
+  int chunks, sms;
 };
 LinearWs linear_ws(const ffdp_linear_params* p, int backward) {
   LinearWs w{};
-  if (!backward) return w;
-  const int n = sms();
-  size_t at = 0;
-  w.gz = at;
-  if (p->act != FFDP_ACT_NONE) at += round256((size_t)p->rows * pad8(p->out) * 2);
-  w.partial = at;
-  w.chunks = linear_grad_chunks((int)p->rows, (int)p->out, n);
-  at += round256((size_t)w.chunks * p->out * 4);
-  w.total = at;
+  w.sms = sms();
+  size_t at = 0, most;
+  if (backward) {
+    w.gz = at;
+    if (p->act != FFDP_ACT_NONE) at += round256((size_t)p->rows * pad8(p->out) * 2);
+    w.partial = at;
+    w.chunks = linear_grad_chunks((int)p->rows, (int)p->out, w.sms);
+    at += round256((size_t)w.chunks * p->out * 4);
+    const size_t gx = linear_plan(p->rows, p->in, p->out, w.sms).partial_bytes;
+    const size_t gw = linear_plan(p->out, p->in, p->rows, w.sms).partial_bytes;
+    most = gx > gw ? gx : gw;
+  } else {
+    most = linear_plan(p->rows, p->out, p->in, w.sms).partial_bytes;
+  }
+  w.product = at;
+  w.total = at + round256(most);
   return w;
 }
 
@@ -324,11 +333,9 @@ extern "C" ffdp_status ffdp_linear_fwd(const void* x, int64_t ldx, const void* w
   if (p->rows == 0) return FFDP_OK;
   LinearArgs a{};
   a.a = x;
-  a.am = ldx;
-  a.ak = 1;
+  a.lda = p->rows > 1 ? ldx : pad8(p->in);
   a.b = w;
-  a.bn = ldw;
-  a.bk = 1;
+  a.ldb = p->out > 1 ? ldw : pad8(p->in);
   a.c = y;
   a.ldc = ldy;
   a.M = (int)p->rows;
@@ -340,7 +347,8 @@ extern "C" ffdp_status ffdp_linear_fwd(const void* x, int64_t ldx, const void* w
   a.z = z;
   a.ldz = ldz;
   a.act = p->act;
-  LAUNCH(launch_linear(dt, a, static_cast<cudaStream_t>(stream)), "linear launch");
+  LAUNCH(launch_linear(dt, a, l.sms, reinterpret_cast<float*>(static_cast<char*>(ws) + l.product), static_cast<cudaStream_t>(stream)),
+         "linear launch");
   return FFDP_OK;
 }
 
@@ -361,6 +369,7 @@ extern "C" ffdp_status ffdp_linear_bwd(const void* x, int64_t ldx, const void* w
   const LinearWs l = linear_ws(p, 1);
   TRY(check_ws(ws, ws_bytes, l.total));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* product = reinterpret_cast<float*>(static_cast<char*>(ws) + l.product);
   const bool act = p->act != FFDP_ACT_NONE;
   const void* gz = gy;
   int64_t ldgz = ldgy;
@@ -387,32 +396,33 @@ extern "C" ffdp_status ffdp_linear_bwd(const void* x, int64_t ldx, const void* w
   if (gx && p->rows) {
     LinearArgs a{};
     a.a = gz;
-    a.am = ldgz;
-    a.ak = 1;
+    a.lda = p->rows > 1 ? ldgz : pad8(p->out);
     a.b = w;
-    a.bn = 1;
-    a.bk = ldw;
+    a.b_mn = 1;
+    a.ldb = p->out > 1 ? ldw : pad8(p->in);
     a.c = gx;
     a.ldc = ldgx;
     a.M = (int)p->rows;
     a.N = (int)p->in;
     a.K = (int)p->out;
-    LAUNCH(launch_linear(dt, a, s), "linear gx launch");
+    LAUNCH(launch_linear(dt, a, l.sms, product, s), "linear gx launch");
   }
-  if (gw) {
+  if (gw && p->rows == 0) {
+    LAUNCH(cudaMemset2DAsync(gw, (size_t)(p->out > 1 ? ldgw : p->in) * 2, 0, (size_t)p->in * 2, (size_t)p->out, s), "gw");
+  } else if (gw) {
     LinearArgs a{};
     a.a = gz;
-    a.am = 1;
-    a.ak = ldgz;
+    a.a_mn = 1;
+    a.lda = p->rows > 1 ? ldgz : pad8(p->out);
     a.b = x;
-    a.bn = 1;
-    a.bk = ldx;
+    a.b_mn = 1;
+    a.ldb = p->rows > 1 ? ldx : pad8(p->in);
     a.c = gw;
     a.ldc = ldgw;
     a.M = (int)p->out;
     a.N = (int)p->in;
     a.K = (int)p->rows;
-    LAUNCH(launch_linear(dt, a, s), "linear gw launch");
+    LAUNCH(launch_linear(dt, a, l.sms, product, s), "linear gw launch");
   }
   return FFDP_OK;
 }

@@ -1,20 +1,24 @@
 // k_linear.cu -- matrix products of the linear operator and its gradients.
 //
-// C[m][n] = sum_k A(m, k) B(n, k): the forward product (x w^T), gx = gz w and
-// gw = gz^T x are this product with other strides.
+// C[m][n] = sum_k A(m, k) B(n, k) + epilogue: the forward product (x w^T), gx =
+// gz w and gw = gz^T x are this product with operands that are contiguous
+// along the contraction (K-major) or across it (MN-major).
+#include <atomic>
+
+#include "ffdp_tc.cuh"
 #include "ffdp_tokens.h"
 
 namespace ffdp {
 
 namespace {
 
-constexpr int kTile = 64, kStep = 16;
+using namespace tc;
 
 __device__ __forceinline__ float act_fwd(int act, float z) {
   switch (act) {
-    case 1: return fmaxf(z, 0.0f);
+    case 1: return z > 0.0f ? z : (z == z ? 0.0f : z);
     case 2: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case 3: return z / (1.0f + expf(-z));
+    case 3: return __fdividef(z, 1.0f + __expf(-z));
     default: return z;
   }
 }
@@ -31,39 +35,328 @@ __device__ __forceinline__ float act_grad(int act, float z) {
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(256) k_linear(const LinearArgs a, int tiles_n) {
-  __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-  const int m0 = blockIdx.x / tiles_n * kTile, n0 = blockIdx.x % tiles_n * kTile;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float c[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += kStep) {
-    for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-      const int ka = a.ak == 1 ? i % kStep : i / kTile, ra = a.ak == 1 ? i / kStep : i % kTile;
-      sa[ka][ra] = m0 + ra < a.M && k0 + ka < a.K ? to_f32<T>(static_cast<const T*>(a.a)[(m0 + ra) * a.am + (k0 + ka) * a.ak]) : 0.0f;
-      const int kb = a.bk == 1 ? i % kStep : i / kTile, rb = a.bk == 1 ? i / kStep : i % kTile;
-      sb[kb][rb] = n0 + rb < a.N && k0 + kb < a.K ? to_f32<T>(static_cast<const T*>(a.b)[(n0 + rb) * a.bn + (k0 + kb) * a.bk]) : 0.0f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kStep; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[i][j] = fmaf(sa[k][ty + 16 * i], sb[k][tx + 16 * j], c[i][j]);
-    __syncthreads();
+template <class T> struct Pair;
+template <> struct Pair<__half> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= a.M || n >= a.N) continue;
-      float z = c[i][j];
-      if (a.bias) z += to_f32<T>(static_cast<const T*>(a.bias)[n]);
-      if (a.z) static_cast<T*>(a.z)[m * a.ldz + n] = from_f32<T>(z);
-      z = act_fwd(a.act, z);
-      if (a.res) z += to_f32<T>(static_cast<const T*>(a.res)[m * a.ldr + n]);
-      static_cast<T*>(a.c)[m * a.ldc + n] = from_f32<T>(z);
+  static __device__ __forceinline__ float2 unpack(uint32_t u) { return __half22float2(*reinterpret_cast<const __half2*>(&u)); }
+};
+template <> struct Pair<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+};
+
+constexpr int kBM = 128, kBK = 64;
+constexpr int kThreads = 384;  // warp 0 loads, warp 1 multiplies, warps 4-11 run the epilogue
+constexpr int kEpiWarps = 8;
+
+__host__ __device__ constexpr int stages(int BN) { return BN == 256 ? 4 : 6; }
+__host__ __device__ constexpr int stage_bytes(int BN) { return (kBM + BN) * kBK * 2; }
+__host__ __device__ constexpr int chunk_cols(int BN) { return BN / 2 < 64 ? BN / 2 : 64; }
+__host__ __device__ constexpr int stage_out_bytes(int BN) { return kEpiWarps * 32 * chunk_cols(BN) * 2; }
+constexpr size_t smem_bytes(int BN) { return 1024 + (size_t)stages(BN) * stage_bytes(BN) + stage_out_bytes(BN) + 256; }
+
+struct Product {
+  int M, N, K;
+  int a_mn, b_mn;      // operand is MN-major
+  int tiles_m, tiles_n, splits, kb;  // kb: contraction blocks of 64 in all
+  uint32_t idesc;
+  // epilogue
+  void* c;
+  int64_t ldc;
+  const void *bias, *res;
+  int64_t ldr;
+  void* z;
+  int64_t ldz;
+  int act;
+  float* partial;      // splits > 1: [tile][split][BN][128] float
+  unsigned* error;
+};
+
+// Work item -> tile and range of contraction blocks.  Tiles run down groups of
+// 16 rows of tiles, so that CTAs in flight share both operands in L2.
+__device__ __forceinline__ void work_item(const Product& p, int w, int* tm, int* tn, int* k0, int* k1) {
+  const int tile = w / p.splits, split = w - tile * p.splits;
+  constexpr int G = 16;
+  const int per = G * p.tiles_n, g = tile / per, first = g * G, rows = min(G, p.tiles_m - first);
+  const int in = tile - g * per;
+  *tm = first + in % rows;
+  *tn = in / rows;
+  *k0 = (int)((int64_t)p.kb * split / p.splits);
+  *k1 = (int)((int64_t)p.kb * (split + 1) / p.splits);
+}
+
+// Epilogue of 32 rows (lane = row) by CW columns held as v[]: bias, activation,
+// residual in 32 bits, one rounding; rows pass through a swizzled patch of
+// shared memory so that global accesses are whole 16-byte pieces of rows.
+template <class T, int CW>
+__device__ __forceinline__ void finish(const Product& p, float* v, int m0, int n0, char* patch, int lane) {
+  constexpr int CH = CW / 8, RP = 32 / CH;  // 16-byte pieces per row, rows per access
+  auto at = [&](int row, int piece) { return reinterpret_cast<uint4*>(patch + row * CW * 2 + ((piece ^ (row % CH)) * 16)); };
+  const int rows = min(32, p.M - m0);
+  auto flush = [&](void* out, int64_t ld) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 32 / RP; ++i) {
+      const int row = i * RP + lane / CH, piece = lane % CH, n = n0 + piece * 8;
+      if (row < rows && n < p.N) {
+        const uint4 u = *at(row, piece);
+        T* o = static_cast<T*>(out) + (int64_t)(m0 + row) * ld + n;
+        if (n + 8 <= p.N) {
+          *reinterpret_cast<uint4*>(o) = u;
+        } else {
+          const T* e = reinterpret_cast<const T*>(&u);
+          for (int k = 0; k < p.N - n; ++k) o[k] = e[k];
+        }
+      }
     }
+    __syncwarp();
+  };
+  auto stage = [&]() {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const float* f = v + 8 * c;
+      *at(lane, c) = make_uint4(Pair<T>::pack(f[0], f[1]), Pair<T>::pack(f[2], f[3]), Pair<T>::pack(f[4], f[5]), Pair<T>::pack(f[6], f[7]));
+    }
+  };
+  if (p.bias) {
+    const T* b = static_cast<const T*>(p.bias) + n0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (n0 + 8 * c + 8 <= p.N) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(b + 8 * c));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = Pair<T>::unpack(w[k]);
+          v[8 * c + 2 * k] += f.x;
+          v[8 * c + 2 * k + 1] += f.y;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (n0 + 8 * c + k < p.N) v[8 * c + k] += to_f32<T>(b[8 * c + k]);
+      }
+    }
+  }
+  if (p.z) {
+    stage();
+    flush(p.z, p.ldz);
+  }
+  switch (p.act) {
+    case 1:
+#pragma unroll
+      for (int i = 0; i < CW; ++i) v[i] = act_fwd(1, v[i]);
+      break;
+    case 2:
+#pragma unroll
+      for (int i = 0; i < CW; ++i) v[i] = act_fwd(2, v[i]);
+      break;
+    case 3:
+#pragma unroll
+      for (int i = 0; i < CW; ++i) v[i] = act_fwd(3, v[i]);
+      break;
+  }
+  if (p.res) {
+#pragma unroll
+    for (int i = 0; i < 32 / RP; ++i) {
+      const int row = i * RP + lane / CH, piece = lane % CH, n = n0 + piece * 8;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (row < rows && n < p.N) {
+        const T* r = static_cast<const T*>(p.res) + (int64_t)(m0 + row) * p.ldr + n;
+        if (n + 8 <= p.N) {
+          u = *reinterpret_cast<const uint4*>(r);
+        } else {
+          T e[8] = {};
+          for (int k = 0; k < p.N - n; ++k) e[k] = r[k];
+          u = *reinterpret_cast<const uint4*>(e);
+        }
+      }
+      *at(row, piece) = u;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const uint4 u = *at(lane, c);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = Pair<T>::unpack(w[k]);
+        v[8 * c + 2 * k] += f.x;
+        v[8 * c + 2 * k + 1] += f.y;
+      }
+    }
+  }
+  stage();
+  flush(p.c, p.ldc);
+}
+
+template <class T, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_product(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const Product p) {
+  constexpr int NST = stages(BN), SB = stage_bytes(BN), CW = chunk_cols(BN);
+  extern __shared__ char raw[];
+  char* base = reinterpret_cast<char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  char* patches = base + NST * SB;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(patches + stage_out_bytes(BN));
+  const uint32_t full = smem_addr(bars), empty = full + 8 * NST, accf = empty + 8 * NST, acce = accf + 16, drain = acce + 16;
+  __shared__ unsigned dead, tmem_slot;
+  const Guard g{&dead, p.error};
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    dead = 0;
+    for (int i = 0; i < NST; ++i) {
+      bar_init(full + 8 * i, 1);
+      bar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(accf + 8 * i, 1);
+      bar_init(acce + 8 * i, kEpiWarps);
+    }
+    bar_init(drain, 1);
+    bar_init_fence();
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 2 * BN);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int items = p.tiles_m * p.tiles_n * p.splits;
+  const uint32_t sm = smem_addr(base);
+
+  if (warp == 0 && elect_one()) {
+    tma_prefetch_map(&ma);
+    tma_prefetch_map(&mb);
+    Ring<NST> r;
+    unsigned issued = 0;
+    bool ok = true;
+    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
+      int tm, tn, k0, k1;
+      work_item(p, w, &tm, &tn, &k0, &k1);
+      for (int k = k0; k < k1; ++k) {
+        if (!bar_wait(empty + 8 * r.slot, r.phase ^ 1u, g)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = full + 8 * r.slot, a = sm + r.slot * SB, b = a + kBM * kBK * 2;
+        bar_expect(bar, SB);
+        if (p.a_mn) {
+#pragma unroll
+          for (int i = 0; i < kBM / 64; ++i) tma_load_2d(a + i * 8192, &ma, tm * kBM + i * 64, k * kBK, bar);
+        } else {
+          tma_load_2d(a, &ma, k * kBK, tm * kBM, bar);
+        }
+        if (p.b_mn) {
+#pragma unroll
+          for (int i = 0; i < BN / 64; ++i) tma_load_2d(b + i * 8192, &mb, tn * BN + i * 64, k * kBK, bar);
+        } else {
+          tma_load_2d(b, &mb, k * kBK, tn * BN, bar);
+        }
+        r.next();
+        ++issued;
+      }
+    }
+    for (unsigned i = issued > NST ? issued - NST : 0; i < issued; ++i) bar_drain(full + 8 * (i % NST), (i / NST) & 1);
+  } else if (warp == 1 && elect_one()) {
+    Ring<NST> r;
+    Ring<2> acc;
+    bool ok = true;
+    const uint32_t step_a = p.a_mn ? 2048 : 32, step_b = p.b_mn ? 2048 : 32;
+    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
+      int tm, tn, k0, k1;
+      work_item(p, w, &tm, &tn, &k0, &k1);
+      if (!bar_wait(acce + 8 * acc.slot, acc.phase ^ 1u, g)) break;
+      fence_after();
+      const uint32_t d = tmem + acc.slot * BN;
+      for (int k = k0; k < k1; ++k) {
+        if (!bar_wait(full + 8 * r.slot, r.phase, g)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t a = sm + r.slot * SB, b = a + kBM * kBK * 2;
+        const uint64_t da = smem_desc(a, 8192, 1024), db = smem_desc(b, 8192, 1024);
+#pragma unroll
+        for (int i = 0; i < kBK / 16; ++i)
+          mma_ss(d, da + ((i * step_a) >> 4), db + ((i * step_b) >> 4), p.idesc, k > k0 || i > 0);
+        mma_commit(empty + 8 * r.slot);
+        r.next();
+      }
+      mma_commit(accf + 8 * acc.slot);
+      acc.next();
+    }
+    mma_commit(drain);
+    bar_drain(drain, 0);
+  } else if (warp >= 4) {
+    const int e = warp - 4, q = e % 4, half = e / 4;
+    char* patch = patches + e * 32 * CW * 2;
+    Ring<2> acc;
+    for (int w = blockIdx.x; w < items; w += gridDim.x) {
+      int tm, tn, k0, k1;
+      work_item(p, w, &tm, &tn, &k0, &k1);
+      if (!bar_wait_warp(accf + 8 * acc.slot, acc.phase, g)) break;
+      fence_after();
+      const uint32_t d = tmem + acc.slot * BN + ((uint32_t)(q * 32) << 16);
+      const int m0 = tm * kBM + q * 32;
+#pragma unroll 1
+      for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += CW) {
+        float v[CW];
+        if (k1 > k0) {
+#pragma unroll
+          for (int i = 0; i < CW; i += 32) tmem_ld32(d + c + i, v + i);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < CW; ++i) v[i] = 0.0f;
+        }
+        if (c + CW == (half + 1) * (BN / 2)) {  // the last read of this accumulator
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(acce + 8 * acc.slot);
+        }
+        if (p.splits > 1) {
+          float* o = p.partial + ((int64_t)w * BN + c) * kBM + q * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < CW; ++i) o[(int64_t)i * kBM] = v[i];
+        } else if (m0 < p.M && tn * BN + c < p.N) {
+          finish<T, CW>(p, v, m0, tn * BN + c, patch, lane);
+        }
+      }
+      acc.next();
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) tmem_free(tmem, 2 * BN);
+}
+
+// Joins the partial products of a split contraction in order of the splits.
+template <class T, int BN>
+__global__ void __launch_bounds__(256) k_product_join(const Product p) {
+  constexpr int CW = 32;
+  __shared__ __align__(128) char patches[8 * 32 * CW * 2];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int per_tile = 4 * (BN / CW);
+  const int u = blockIdx.x * 8 + warp, tile = u / per_tile, part = u - tile * per_tile;
+  if (tile >= p.tiles_m * p.tiles_n) return;
+  int tm, tn, k0, k1;
+  work_item(p, tile * p.splits, &tm, &tn, &k0, &k1);
+  const int q = part % 4, c = part / 4 * CW, m0 = tm * kBM + q * 32, n0 = tn * BN + c;
+  if (m0 >= p.M || n0 >= p.N) return;
+  float v[CW] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    const float* o = p.partial + (((int64_t)tile * p.splits + s) * BN + c) * kBM + q * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < CW; ++i) v[i] += o[(int64_t)i * kBM];
+  }
+  finish<T, CW>(p, v, m0, n0, patches + warp * 32 * CW * 2, lane);
 }
 
 // One thread per column and chunk of rows.
@@ -93,15 +386,91 @@ __global__ void __launch_bounds__(128) k_linear_gb(const LinearGradArgs a) {
   static_cast<T*>(a.gb)[n] = from_f32<T>(sum);
 }
 
+template <class T, int BN>
+cudaError_t run_product(const CUtensorMap& ma, const CUtensorMap& mb, const Product& p, int grid, cudaStream_t s) {
+  static std::atomic<unsigned long long> ready{0};  // one bit per device: shared-memory size granted
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k_product<T, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(BN));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  note_launch_begin("k_product", s);
+  k_product<T, BN><<<grid, kThreads, smem_bytes(BN), s>>>(ma, mb, p);
+  note_launch_end(s);
+  if (p.splits > 1) {
+    const int units = p.tiles_m * p.tiles_n * 4 * (BN / 32);
+    note_launch_begin("k_product_join", s);
+    k_product_join<T, BN><<<(units + 7) / 8, 256, 0, s>>>(p);
+    note_launch_end(s);
+  }
+  return cudaGetLastError();
+}
+
+int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
 }  // namespace
 
-cudaError_t launch_linear(int dt, const LinearArgs& a, cudaStream_t s) {
-  const int tn = (a.N + kTile - 1) / kTile;
-  const int64_t grid = (int64_t)((a.M + kTile - 1) / kTile) * tn;
-  note_launch_begin("k_linear", s);
-  FFDP_TOK_SWITCH16(dt, T, (k_linear<T><<<(unsigned)grid, 256, 0, s>>>(a, tn)));
-  note_launch_end(s);
-  return cudaGetLastError();
+// The tile is 128 x 256 where that gives every SM a tile (the least operand
+// traffic per product), else 128 x 128 or 128 x 64; a product with still fewer
+// tiles than SMs splits its contraction, at least 4 blocks of 64 per split.
+LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int sms) {
+  LinearPlan l{};
+  const int64_t tm = (M + kBM - 1) / kBM;
+  l.bn = 256;
+  while (l.bn > 64 && tm * ((N + l.bn - 1) / l.bn) < sms) l.bn >>= 1;
+  const int64_t tiles = tm * ((N + l.bn - 1) / l.bn), kb = (K + kBK - 1) / kBK;
+  int64_t s = 1;
+  if (tiles * 2 <= sms) s = sms / tiles;
+  if (s > kb / 4) s = kb / 4;
+  l.splits = (int)(s < 1 ? 1 : s);
+  l.partial_bytes = l.splits > 1 ? (size_t)tiles * l.splits * l.bn * kBM * 4 : 0;
+  return l;
+}
+
+cudaError_t launch_linear(int dt, const LinearArgs& a, int sms, float* partial, cudaStream_t s) {
+  const LinearPlan l = linear_plan(a.M, a.N, a.K, sms);
+  CUtensorMap ma, mb;
+  auto map = [&](CUtensorMap* m, const void* ptr, int mn_major, int64_t ld, int mn, int box_mn) {
+    const int64_t ext_k[2] = {a.K, mn}, ext_mn[2] = {mn, a.K};
+    const int box_k[2] = {kBK, box_mn}, box_m[2] = {64, kBK};
+    return make_tensor_map(m, dt, ptr, 2, mn_major ? ext_mn : ext_k, &ld, mn_major ? box_m : box_k);
+  };
+  cudaError_t e = map(&ma, a.a, a.a_mn, a.lda, a.M, kBM);
+  if (e == cudaSuccess) e = map(&mb, a.b, a.b_mn, a.ldb, a.N, l.bn);
+  if (e != cudaSuccess) return e;
+  Product p{};
+  p.M = a.M;
+  p.N = a.N;
+  p.K = a.K;
+  p.a_mn = a.a_mn;
+  p.b_mn = a.b_mn;
+  p.tiles_m = div_up(a.M, kBM);
+  p.tiles_n = div_up(a.N, l.bn);
+  p.splits = l.splits;
+  p.kb = div_up(a.K, kBK);
+  p.idesc = mma_idesc(dt == 2, a.a_mn, a.b_mn, kBM, l.bn);
+  p.c = a.c;
+  p.ldc = a.ldc;
+  p.bias = a.bias;
+  p.res = a.res;
+  p.ldr = a.ldr;
+  p.z = a.z;
+  p.ldz = a.ldz;
+  p.act = a.act;
+  p.partial = partial;
+  e = device_error_word(&p.error);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+  const int grid = (int)(items < sms ? items : sms);
+  FFDP_TOK_SWITCH16(dt, T, {
+    if (l.bn == 256) return run_product<T, 256>(ma, mb, p, grid, s);
+    if (l.bn == 128) return run_product<T, 128>(ma, mb, p, grid, s);
+    return run_product<T, 64>(ma, mb, p, grid, s);
+  });
 }
 
 int linear_grad_chunks(int M, int N, int sms) {
@@ -123,6 +492,39 @@ cudaError_t launch_linear_grad(int dt, const LinearGradArgs& a, cudaStream_t s) 
     note_launch_end(s);
   }
   return cudaGetLastError();
+}
+
+namespace {
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+std::atomic<EncodeFn> g_encode{nullptr};
+}  // namespace
+
+cudaError_t make_tensor_map(CUtensorMap* m, int dt, const void* p, int rank, const int64_t* extent, const int64_t* stride,
+                            const int* box) {
+  EncodeFn f = g_encode.load(std::memory_order_relaxed);
+  if (!f) {
+    void* sym = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !sym) return cudaErrorNotSupported;
+    f = reinterpret_cast<EncodeFn>(sym);
+    g_encode.store(f, std::memory_order_relaxed);
+  }
+  cuuint64_t ext[5], str[4];
+  cuuint32_t bx[5], one[5];
+  for (int i = 0; i < rank; ++i) {
+    ext[i] = (cuuint64_t)extent[i];
+    bx[i] = (cuuint32_t)box[i];
+    one[i] = 1;
+    if (i + 1 < rank) str[i] = (cuuint64_t)stride[i] * 2;
+  }
+  const CUresult r = f(m, dt == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+                       const_cast<void*>(p), ext, str, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 }  // namespace ffdp
