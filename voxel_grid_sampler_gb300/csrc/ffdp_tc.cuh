@@ -58,7 +58,7 @@ struct Guard {
   unsigned* error;
 };
 
-__device__ __noinline__ bool bar_wait_slow(uint32_t bar, unsigned parity, const Guard& g) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t bar, unsigned parity, const Guard& g) {
   const unsigned long long t0 = now_ns();
   while (!bar_try(bar, parity)) {
     if (*g.dead) return false;

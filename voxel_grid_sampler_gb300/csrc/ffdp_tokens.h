@@ -66,7 +66,13 @@ struct AttnArgs {
   int64_t doc_q_sb, doc_k_sb;
   const int* prefix;
 };
-cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, cudaStream_t s);
+// Query tiles of the forward pass, their packing and splits, workspace parts.
+struct AttnPlan {
+  int packed, rh, gb, tiles, pairs, splits, nq, nk;
+  size_t ranges_bytes, part_bytes;
+};
+AttnPlan attention_plan(const AttnArgs& a, int sms);
+cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, int sms, void* ws, cudaStream_t s);
 cudaError_t launch_attention_bwd(int dt, const AttnArgs& a, cudaStream_t s);
 
 // C[m][n] = sum_k A(m, k) B(n, k).  An operand is K-major (rows m or n of K

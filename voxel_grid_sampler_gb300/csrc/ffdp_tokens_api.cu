@@ -194,7 +194,12 @@ ffdp_status fill_attention(const ffdp_attention_params* p, const ffdp_attention_
 }
 
 size_t attention_ws(const ffdp_attention_params* p, int backward) {
-  if (!backward) return 256;
+  AttnArgs a{};
+  fill_attention(p, nullptr, a);
+  if (!backward) {
+    const AttnPlan l = attention_plan(a, sms());
+    return 256 + l.ranges_bytes + l.part_bytes;
+  }
   return 256 + round256((size_t)p->batch * p->q_heads * p->q_len * 4);
 }
 
@@ -223,7 +228,7 @@ extern "C" ffdp_status ffdp_attention_fwd(const ffdp_heads* q, const ffdp_heads*
   TRY(check_ws(ws, ws_bytes, attention_ws(p, 0)));
   a.lse = lse;
   if (a.B == 0 || a.Sq == 0) return FFDP_OK;
-  LAUNCH(launch_attention_fwd(dt, a, static_cast<cudaStream_t>(stream)), "attention forward launch");
+  LAUNCH(launch_attention_fwd(dt, a, sms(), ws, static_cast<cudaStream_t>(stream)), "attention forward launch");
   return FFDP_OK;
 }
 

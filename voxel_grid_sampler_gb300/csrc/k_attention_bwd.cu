@@ -1,7 +1,7 @@
-// k_attention.cu -- attention over volume tokens, forward and backward.
+// k_attention_bwd.cu -- attention over volume tokens, backward.
 //
-// One warp per query row (forward, gq) or key row (gk, gv): a dot product per
-// pair across the lanes, a running maximum and sum for the softmax.
+// One warp per query row (gq) or key row (gk, gv): a dot product per pair
+// across the lanes.
 #include "ffdp_tokens.h"
 
 namespace ffdp {
@@ -69,31 +69,6 @@ __device__ __forceinline__ float score(const AttnArgs& a, int b, int h, int i, i
 }
 
 template <class T>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_fwd(const AttnArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-  if (r >= (int64_t)a.B * a.Hq * a.Sq) return;
-  const int i = (int)(r % a.Sq), h = (int)(r / a.Sq % a.Hq), b = (int)(r / a.Sq / a.Hq), g = h / a.G;
-  float q[kE], o[kE] = {}, m = -INFINITY, l = 0.0f, x;
-  row<T>(a.q, b, i, h, a.D, q);
-  for (int j = 0; j < a.Sk; ++j) {
-    if (!visible(a, b, i, j)) continue;
-    float k[kE], v[kE];
-    row<T>(a.k, b, j, g, a.D, k);
-    const float s = score(a, b, h, i, j, dot(q, k), &x);
-    const float mn = fmaxf(m, s), w = m == mn ? 1.0f : expf(m - mn), p = expf(s - mn);
-    row<T>(a.v, b, j, g, a.D, v);
-    l = l * w + p;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = fmaf(p, v[e], o[e] * w);
-    m = mn;
-  }
-#pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] = l == 0.0f ? 0.0f : o[e] / l;
-  put<T>(a.o, b, i, h, a.D, o);
-  if (a.lse && (threadIdx.x & 31) == 0) a.lse[r] = l == 0.0f ? -INFINITY : m + logf(l);
-}
-
-template <class T>
 __global__ void __launch_bounds__(kWarps * 32) k_attn_bwd_q(const AttnArgs a) {
   const int64_t r = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
   if (r >= (int64_t)a.B * a.Hq * a.Sq) return;
@@ -147,13 +122,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_attn_bwd_kv(const AttnArgs a) {
 unsigned blocks(int64_t rows) { return (unsigned)((rows + kWarps - 1) / kWarps); }
 
 }  // namespace
-
-cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, cudaStream_t s) {
-  note_launch_begin("k_attn_fwd", s);
-  FFDP_TOK_SWITCH16(dt, T, (k_attn_fwd<T><<<blocks((int64_t)a.B * a.Hq * a.Sq), kWarps * 32, 0, s>>>(a)));
-  note_launch_end(s);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_attention_bwd(int dt, const AttnArgs& a, cudaStream_t s) {
   if (a.Sq) {
