@@ -65,29 +65,30 @@ __device__ __forceinline__ int prefix_of(const AttnArgs& a, int b) { return a.pr
 // Tile pair codes: nothing visible, everything visible, some pairs masked.
 enum { kSkip = 0, kFull = 1, kMasked = 2 };
 
-// Queries [i0, i1) against key tile j.
-__device__ __forceinline__ int pair_code(const AttnArgs& a, int prefix, int b, int i0, int i1, int j, const DocRange* dq,
-                                         const DocRange* dk) {
+// Queries [i0, i1) against keys [k0, k1), each range inside one tile of 128;
+// k1 may pass the last key.
+__device__ __forceinline__ int pair_code(const AttnArgs& a, int prefix, int b, int i0, int i1, int k0, int k1,
+                                         const DocRange* dq, const DocRange* dk) {
   if (i0 >= i1) return kSkip;
-  if (j * kTile >= key_limit(a, prefix, i1 - 1)) return kSkip;
-  int code = (j + 1) * kTile > key_limit(a, prefix, i0) ? kMasked : kFull;
+  if (k0 >= key_limit(a, prefix, i1 - 1)) return kSkip;
+  int code = k1 > key_limit(a, prefix, i0) ? kMasked : kFull;
   if (dq) {
     const DocRange q = dq[(int64_t)b * ((a.Sq + kTile - 1) / kTile) + i0 / kTile];
-    const DocRange k = dk[(int64_t)b * ((a.Sk + kTile - 1) / kTile) + j];
+    const DocRange k = dk[(int64_t)b * ((a.Sk + kTile - 1) / kTile) + k0 / kTile];
     if (docs_apart(q, k)) return kSkip;
     if (!docs_one(q, k)) code = kMasked;
   }
   return code;
 }
 
-// A row of a [128][64 channels per panel] tile in shared memory holds an
+// A row of a [rows][64 channels per panel] tile in shared memory holds an
 // infinity or NaN: zero it (its products with masked weights must vanish) and
 // say so.
 template <class T>
-__device__ __forceinline__ bool clear_bad_row(char* tile, int panels, int row) {
+__device__ __forceinline__ bool clear_bad_row(char* tile, int panels, int panel_bytes, int row) {
   bool bad = false;
   for (int p = 0; p < panels; ++p) {
-    const uint4* r = reinterpret_cast<const uint4*>(tile + p * kPanel + row * 128);
+    const uint4* r = reinterpret_cast<const uint4*>(tile + p * panel_bytes + row * 128);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       const uint4 u = r[c];
@@ -96,7 +97,7 @@ __device__ __forceinline__ bool clear_bad_row(char* tile, int panels, int row) {
   }
   if (bad)
     for (int p = 0; p < panels; ++p) {
-      uint4* r = reinterpret_cast<uint4*>(tile + p * kPanel + row * 128);
+      uint4* r = reinterpret_cast<uint4*>(tile + p * panel_bytes + row * 128);
 #pragma unroll
       for (int c = 0; c < 8; ++c) r[c] = make_uint4(0, 0, 0, 0);
     }

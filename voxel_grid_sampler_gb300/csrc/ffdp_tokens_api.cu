@@ -200,7 +200,7 @@ size_t attention_ws(const ffdp_attention_params* p, int backward) {
     const AttnPlan l = attention_plan(a, sms());
     return 256 + l.ranges_bytes + l.part_bytes;
   }
-  return 256 + round256((size_t)p->batch * p->q_heads * p->q_len * 4);
+  return 256 + attention_bwd_bytes(a);
 }
 
 }  // namespace
@@ -253,9 +253,8 @@ extern "C" ffdp_status ffdp_attention_bwd(const ffdp_heads* q, const ffdp_heads*
   if (a.B * (int64_t)a.Sq > 0 && (!lse || !aligned(lse, 4))) FAIL(FFDP_ERR_INVALID_ARGUMENT, "lse must be non-null and 4-byte aligned");
   TRY(check_ws(ws, ws_bytes, attention_ws(p, 1)));
   a.lse = const_cast<float*>(lse);
-  a.delta = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
   if (a.B == 0) return FFDP_OK;
-  LAUNCH(launch_attention_bwd(dt, a, static_cast<cudaStream_t>(stream)), "attention backward launch");
+  LAUNCH(launch_attention_bwd(dt, a, ws, static_cast<cudaStream_t>(stream)), "attention backward launch");
   return FFDP_OK;
 }
 

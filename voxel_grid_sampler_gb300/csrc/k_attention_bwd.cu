@@ -1,140 +1,516 @@
 // k_attention_bwd.cu -- attention over volume tokens, backward.
 //
-// One warp per query row (gq) or key row (gk, gv): a dot product per pair
-// across the lanes.
-#include "ffdp_tokens.h"
+// With P = exp(score - lse), dP = go v^T, delta = sum_d go o and dS = P (dP -
+// delta) score':  gv = P^T go,  gk = scale dS^T q,  gq = scale dS k.
+// Two passes of one kernel recompute P: in the first a CTA owns 128 keys of a
+// key head and walks the queries of its query heads (gk, gv accumulate in
+// TMEM), in the second it owns 128 queries and walks the keys (gq).  Each
+// gradient is summed by one CTA in a fixed order, with no atomics and no
+// 32-bit gradient buffer, for two of seven products done twice.
+//
+// Walked tokens come in subtiles of 64, two in flight: S = R1 T1^T and dP = R2
+// T2^T (R: resident rows, T: walked rows) go to TMEM, a warpgroup per subtile
+// (one resident row per thread) turns them into P and dS in 16 bits in the
+// same columns, which are the A operands of the accumulating products.  Warps:
+// 0-3 and 4-7 even and odd subtiles, 8 loads (TMA), 9 multiplies, 10 prepares
+// each subtile's lse, delta, positions, documents and non-finite rows.
+#include <atomic>
+
+#include "ffdp_attention.cuh"
 
 namespace ffdp {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kE = 4;  // channels per lane (head_dim <= 128)
+using namespace tc;
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+constexpr int kThreads = 384;
+constexpr int kSub = 64;                // walked tokens per step
+constexpr int kSubPanel = kSub * 128;   // bytes of 64 channels of a subtile
+constexpr int kStages = 4;
+constexpr unsigned kTmemCols = 512;
 
-template <class T>
-__device__ __forceinline__ void row(const HeadsView& t, int b, int s, int h, int D, float* f) {
-  const T* p = static_cast<const T*>(t.p) + b * t.sb + s * t.st + h * t.sh;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    const int c = (threadIdx.x & 31) + 32 * e;
-    f[e] = c < D ? to_f32<T>(p[c]) : 0.0f;
+struct BwdArgs {
+  AttnArgs a;
+  const DocRange *dq, *dk;
+  int panels;
+  uint32_t idesc_s, idesc_dp, idesc_acc;
+  float c;             // |scale| log2 e
+  float cap_in, cap2;  // 2 log2 e |scale| / cap, cap log2 e
+  unsigned* error;
+};
+
+// Per slot of walked tokens.
+struct alignas(16) Aux {
+  float lse[kSub], delta[kSub];  // keys resident: of the walked queries (base-2 lse)
+  float pos[3][kSub];            // scaled by the head's slopes
+  int doc[kSub], limit[kSub];    // limit: keys resident, first key the query does not see
+  unsigned bad[2];
+};
+
+template <class T, int AXES, bool CAP, bool KV>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_bwd(const __grid_constant__ CUtensorMap mr1, const __grid_constant__ CUtensorMap mr2,
+               const __grid_constant__ CUtensorMap mt1, const __grid_constant__ CUtensorMap mt2, const BwdArgs f) {
+  extern __shared__ char raw[];
+  char* base = reinterpret_cast<char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  __shared__ uint64_t bars[1 + 3 * kStages + 6 + 2];
+  __shared__ unsigned dead, tmem_slot;
+  __shared__ uint8_t codes[kMaxCodes];
+  __shared__ __align__(16) Aux aux[kStages];
+  const AttnArgs& a = f.a;
+  const int res_bytes = f.panels * kPanel, sub_bytes = f.panels * kSubPanel;
+  char *r1 = base, *r2 = r1 + res_bytes, *st = r2 + res_bytes;  // slot s: T1 then T2
+  const uint32_t rfull = smem_addr(bars), tfull = rfull + 8, tempty = tfull + 8 * kStages, ready = tempty + 8 * kStages,
+                 sfull = ready + 8 * kStages, pfull = sfull + 16, done = pfull + 16, accfull = done + 16, drain = accfull + 8;
+  const Guard guard{&dead, f.error};
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  // this CTA's resident tile; causal calls begin with the longest walks
+  const int H = KV ? a.Hk : a.Hq, tiles = ((KV ? a.Sk : a.Sq) + kTile - 1) / kTile;
+  int tile, bh;
+  if (a.causal) {
+    tile = blockIdx.x / (a.B * H);
+    bh = blockIdx.x - tile * (a.B * H);
+    if (!KV) tile = tiles - 1 - tile;
+  } else {
+    bh = blockIdx.x / tiles;
+    tile = blockIdx.x - bh * tiles;
   }
-}
-
-template <class T>
-__device__ __forceinline__ void put(const HeadsView& t, int b, int s, int h, int D, const float* f) {
-  T* p = static_cast<T*>(t.p) + b * t.sb + s * t.st + h * t.sh;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    const int c = (threadIdx.x & 31) + 32 * e;
-    if (c < D) p[c] = from_f32<T>(f[e]);
-  }
-}
-
-__device__ __forceinline__ float dot(const float* a, const float* b) {
-  float s = 0.0f;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) s = fmaf(a[e], b[e], s);
-  return warp_sum(s);
-}
-
-__device__ __forceinline__ bool visible(const AttnArgs& a, int b, int i, int j) {
-  if (a.causal && j > i + a.Sk - a.Sq && (!a.prefix || j >= a.prefix[b])) return false;
-  if (a.doc_q) {
-    const int d = a.doc_q[b * a.doc_q_sb + i];
-    if (d < 0 || d != a.doc_k[b * a.doc_k_sb + j]) return false;
-  }
-  return true;
-}
-
-// score of a pair from its product, and d score / d (scale product)
-__device__ __forceinline__ float score(const AttnArgs& a, int b, int h, int i, int j, float qk, float* slope) {
-  float s = qk * a.scale;
-  *slope = 1.0f;
-  if (a.cap > 0.0f) {
-    const float t = tanhf(s / a.cap);
-    s = a.cap * t;
-    *slope = 1.0f - t * t;
-  }
-  for (int x = 0; x < a.axes; ++x)
-    s -= a.slopes[h * a.axes + x] *
-         fabsf(a.pos_q[b * a.pos_q_sb + (int64_t)i * a.axes + x] - a.pos_k[b * a.pos_k_sb + (int64_t)j * a.axes + x]);
-  return s;
-}
-
-template <class T>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_bwd_q(const AttnArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-  if (r >= (int64_t)a.B * a.Hq * a.Sq) return;
-  const int i = (int)(r % a.Sq), h = (int)(r / a.Sq % a.Hq), b = (int)(r / a.Sq / a.Hq), g = h / a.G;
-  float q[kE], o[kE], go[kE], gq[kE] = {};
-  row<T>(a.q, b, i, h, a.D, q);
-  row<T>(a.o, b, i, h, a.D, o);
-  row<T>(a.go, b, i, h, a.D, go);
-  const float delta = dot(o, go), lse = a.lse[r];
-  if ((threadIdx.x & 31) == 0) a.delta[r] = delta;
-  for (int j = 0; j < a.Sk; ++j) {
-    if (!visible(a, b, i, j)) continue;
-    float k[kE], v[kE], slope;
-    row<T>(a.k, b, j, g, a.D, k);
-    row<T>(a.v, b, j, g, a.D, v);
-    const float p = expf(score(a, b, h, i, j, dot(q, k), &slope) - lse);
-    const float ds = p * (dot(go, v) - delta) * slope * a.scale;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) gq[e] = fmaf(ds, k[e], gq[e]);
-  }
-  put<T>(a.gq, b, i, h, a.D, gq);
-}
-
-template <class T>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_bwd_kv(const AttnArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32;
-  if (r >= (int64_t)a.B * a.Hk * a.Sk) return;
-  const int j = (int)(r % a.Sk), g = (int)(r / a.Sk % a.Hk), b = (int)(r / a.Sk / a.Hk);
-  float k[kE], v[kE], gk[kE] = {}, gv[kE] = {};
-  row<T>(a.k, b, j, g, a.D, k);
-  row<T>(a.v, b, j, g, a.D, v);
-  for (int h = g * a.G; h < (g + 1) * a.G; ++h)
-    for (int i = 0; i < a.Sq; ++i) {
-      if (!visible(a, b, i, j)) continue;
-      float q[kE], go[kE], slope;
-      row<T>(a.q, b, i, h, a.D, q);
-      row<T>(a.go, b, i, h, a.D, go);
-      const int64_t at = ((int64_t)b * a.Hq + h) * a.Sq + i;
-      const float p = expf(score(a, b, h, i, j, dot(q, k), &slope) - a.lse[at]);
-      const float ds = p * (dot(go, v) - a.delta[at]) * slope * a.scale;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        gv[e] = fmaf(p, go[e], gv[e]);
-        gk[e] = fmaf(ds, q[e], gk[e]);
-      }
+  const int b = bh / H, hr = bh - b * H;          // resident head
+  const int g = KV ? hr : hr / a.G;               // key head
+  const int heads = KV ? a.G : 1, h0 = KV ? hr * a.G : hr;  // query heads walked
+  const int prefix = prefix_of(a, b);
+  const int x0 = tile * kTile, x1 = min(x0 + kTile, KV ? a.Sk : a.Sq);
+  const int walk = KV ? a.Sq : a.Sk, nsub = (walk + kSub - 1) / kSub;
+  auto code_of = [&](int n) {
+    const int y0 = n * kSub, y1 = min(y0 + kSub, walk);
+    return KV ? pair_code(a, prefix, b, y0, y1, x0, x0 + kTile, f.dq, f.dk)
+              : pair_code(a, prefix, b, x0, x1, y0, y0 + kSub, f.dq, f.dk);
+  };
+  for (int n = threadIdx.x; n < min(nsub, kMaxCodes); n += kThreads) codes[n] = (uint8_t)code_of(n);
+  if (threadIdx.x == 0) {
+    dead = 0;
+    bar_init(rfull, 1);
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(tfull + 8 * i, 1);
+      bar_init(tempty + 8 * i, 1);
+      bar_init(ready + 8 * i, 1);
     }
-  put<T>(a.gk, b, j, g, a.D, gk);
-  put<T>(a.gv, b, j, g, a.D, gv);
+    for (int s = 0; s < 2; ++s) {
+      bar_init(sfull + 8 * s, 1);
+      bar_init(pfull + 8 * s, 4);
+      bar_init(done + 8 * s, 1);
+    }
+    bar_init(accfull, 1);
+    bar_init(drain, 1);
+    bar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  // TMEM columns: two stages of S (64) and dP (64), then the accumulators
+  auto s_at = [&](int s) { return tmem + s * 128; };
+  auto dp_at = [&](int s) { return tmem + s * 128 + 64; };
+  const uint32_t acc1 = tmem + 256, acc2 = tmem + 384;  // gv; gk or gq
+
+  // The walk: subtiles of each query head in turn, skipping what nothing sees.
+  struct Step {
+    int head, n, code;
+  };
+  auto advance = [&](Step s) {  // first subtile at or after s with visible pairs; head == heads: none
+    for (;;) {
+      if (s.n >= nsub) {
+        s.n = 0;
+        if (++s.head >= heads) break;
+      }
+      s.code = s.n < kMaxCodes ? codes[s.n] : code_of(s.n);
+      if (s.code) break;
+      ++s.n;
+    }
+    return s;
+  };
+  auto next = [&](Step s) {
+    ++s.n;
+    return advance(s);
+  };
+  Step cur = advance(Step{nsub > 0 ? 0 : heads, 0, 0});
+
+  if (warp == 8 && elect_one()) {
+    if (cur.head < heads) {
+      bar_expect(rfull, 2 * res_bytes);
+      for (int p = 0; p < f.panels; ++p) {
+        tma_load_4d(smem_addr(r1 + p * kPanel), &mr1, p * 64, x0, hr, b, rfull);
+        tma_load_4d(smem_addr(r2 + p * kPanel), &mr2, p * 64, x0, hr, b, rfull);
+      }
+      Ring<kStages> r;
+      unsigned issued = 0;
+      for (; cur.head < heads; cur = next(cur)) {
+        if (!bar_wait(tempty + 8 * r.slot, r.phase ^ 1u, guard)) break;
+        const uint32_t bar = tfull + 8 * r.slot, dst = smem_addr(st + r.slot * 2 * sub_bytes);
+        const int ht = KV ? h0 + cur.head : g;
+        bar_expect(bar, 2 * sub_bytes);
+        for (int p = 0; p < f.panels; ++p) {
+          tma_load_4d(dst + p * kSubPanel, &mt1, p * 64, cur.n * kSub, ht, b, bar);
+          tma_load_4d(dst + sub_bytes + p * kSubPanel, &mt2, p * 64, cur.n * kSub, ht, b, bar);
+        }
+        r.next();
+        ++issued;
+      }
+      bar_drain(rfull, 0);
+      for (unsigned i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+        bar_drain(tfull + 8 * (i % kStages), (i / kStages) & 1);
+    }
+  } else if (warp == 9 && elect_one()) {
+    const int ksteps = (a.D + 15) / 16;
+    Ring<kStages> ts, ta;       // slots of the scores' and of the accumulating products
+    unsigned n = 0;             // subtiles whose scores were issued
+    auto scores = [&]() {
+      const int s = n & 1;
+      const uint32_t t = smem_addr(st + ts.slot * 2 * sub_bytes);
+      for (int k = 0; k < ksteps; ++k) {
+        const uint32_t ro = (k / 4) * kPanel + (k % 4) * 32, to = (k / 4) * kSubPanel + (k % 4) * 32;
+        mma_ss(s_at(s), smem_desc(smem_addr(r1) + ro, 16, 1024), smem_desc(t + to, 16, 1024), f.idesc_s, k > 0);
+      }
+      for (int k = 0; k < ksteps; ++k) {
+        const uint32_t ro = (k / 4) * kPanel + (k % 4) * 32, to = (k / 4) * kSubPanel + (k % 4) * 32;
+        mma_ss(dp_at(s), smem_desc(smem_addr(r2) + ro, 16, 1024), smem_desc(t + sub_bytes + to, 16, 1024), f.idesc_dp, k > 0);
+      }
+      mma_commit(sfull + 8 * s);
+      ts.next();
+      ++n;
+    };
+    bool ok = cur.head < heads && bar_wait(rfull, 0, guard) && bar_wait(tfull, 0, guard);
+    if (ok) {
+      fence_after();
+      scores();
+    }
+    for (unsigned m = 0; ok; ++m) {  // m: subtile whose P and dS are consumed
+      cur = next(cur);
+      const bool more = cur.head < heads;
+      if (more) {
+        // the stage's previous P and dS must have been read
+        ok = bar_wait(tfull + 8 * ts.slot, ts.phase, guard) &&
+             (n < 2 || bar_wait(done + 8 * (n & 1), ((n - 2) / 2) & 1u, guard));
+        if (!ok) break;
+        fence_after();
+        scores();
+      }
+      const int s = m & 1;
+      if (!(ok = bar_wait(ready + 8 * ta.slot, ta.phase, guard) && bar_wait(pfull + 8 * s, (m / 2) & 1u, guard))) break;
+      fence_after();
+      const uint32_t t = smem_addr(st + ta.slot * 2 * sub_bytes);
+#pragma unroll
+      for (int k = 0; k < kSub / 16; ++k) {
+        if (KV) mma_ts(acc1, s_at(s) + k * 8, smem_desc(t + sub_bytes + k * 2048, kSubPanel, 1024), f.idesc_acc, m > 0 || k > 0);
+        mma_ts(acc2, dp_at(s) + k * 8, smem_desc(t + k * 2048, kSubPanel, 1024), f.idesc_acc, m > 0 || k > 0);
+      }
+      mma_commit(done + 8 * s);
+      mma_commit(tempty + 8 * ta.slot);
+      ta.next();
+      if (!more) break;
+    }
+    mma_commit(accfull);
+    mma_commit(drain);
+    bar_drain(drain, 0);
+  } else if (warp == 10) {
+    Ring<kStages> r;
+    for (; cur.head < heads; cur = next(cur)) {
+      const int h = h0 + cur.head;
+      const bool masked = cur.code == kMasked;
+      float lse[2], delta[2], pos[2][3];
+      int doc[2], limit[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int y = cur.n * kSub + i * 32 + lane;
+        const bool in = y < walk;
+        if (KV) {
+          const int64_t at = ((int64_t)b * a.Hq + h) * a.Sq + y;
+          const float v = in ? a.lse[at] : INFINITY;
+          lse[i] = v == -INFINITY ? INFINITY : v * kLog2e;  // no key seen: P = 2^(score - inf) = 0
+          delta[i] = in && v != -INFINITY ? a.delta[at] : 0.0f;
+          limit[i] = masked ? key_limit(a, prefix, y) : 0;
+        }
+        if (AXES) {
+          const float* pp = KV ? a.pos_q + b * a.pos_q_sb : a.pos_k + b * a.pos_k_sb;
+#pragma unroll
+          for (int x = 0; x < 3; ++x)
+            pos[i][x] = x < a.axes && in ? pp[(int64_t)y * a.axes + x] * (a.slopes[h * a.axes + x] * kLog2e) : 0.0f;
+        }
+        doc[i] = a.doc_q && masked && in ? (KV ? a.doc_q[b * a.doc_q_sb + y] : a.doc_k[b * a.doc_k_sb + y]) : -1;
+      }
+      if (!bar_wait_warp(tfull + 8 * r.slot, r.phase, guard)) break;
+      Aux& x = aux[r.slot];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int e = i * 32 + lane;
+        if (KV) {
+          x.lse[e] = lse[i];
+          x.delta[e] = delta[i];
+          x.limit[e] = limit[i];
+        }
+        if (AXES) {
+#pragma unroll
+          for (int c = 0; c < 3; ++c) x.pos[c][e] = pos[i][c];
+        }
+        x.doc[e] = doc[i];
+        if (masked) {
+          char* t = st + r.slot * 2 * sub_bytes;
+          bool bad = clear_bad_row<T>(t, f.panels, kSubPanel, e);
+          if (KV) bad |= clear_bad_row<T>(t + sub_bytes, f.panels, kSubPanel, e);
+          const unsigned m = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) x.bad[i] = m;
+        }
+      }
+      if (masked) fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(ready + 8 * r.slot);
+      r.next();
+    }
+  } else if (warp < 8) {
+    const int wg = warp / 4, row = (warp % 4) * 32 + lane, x = x0 + row;
+    const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
+    const bool valid = x < x1;
+    const int xc = valid ? x : x0;
+    float raw_pos[3], pos[3] = {};
+    if (AXES) {
+      const float* pp = KV ? a.pos_k + b * a.pos_k_sb : a.pos_q + b * a.pos_q_sb;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) raw_pos[i] = i < a.axes ? pp[(int64_t)xc * a.axes + i] : 0.0f;
+    }
+    const int doc = a.doc_q ? (KV ? a.doc_k[b * a.doc_k_sb + xc] : a.doc_q[b * a.doc_q_sb + xc]) : 0;
+    const int limit = KV ? 0 : key_limit(a, prefix, xc);
+    float lse_r = 0.0f, delta_r = 0.0f;
+    if (!KV) {
+      const int64_t at = ((int64_t)b * a.Hq + h0) * a.Sq + xc;
+      const float v = a.lse[at];
+      lse_r = v == -INFINITY ? INFINITY : v * kLog2e;
+      delta_r = v == -INFINITY ? 0.0f : a.delta[at];
+    }
+    int head = -1;
+    unsigned n = 0;
+    Ring<kStages> r;
+    bool ok = true;
+    for (; cur.head < heads; cur = next(cur), ++n, r.next()) {
+      if ((int)(n & 1) != wg) continue;
+      if (AXES && head != cur.head) {
+        head = cur.head;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          pos[i] = i < a.axes ? raw_pos[i] * (a.slopes[(h0 + head) * a.axes + i] * kLog2e) : 0.0f;
+      }
+      if (!(ok = bar_wait_warp(ready + 8 * r.slot, r.phase, guard))) break;
+      if (!(ok = bar_wait_warp(sfull + 8 * wg, (n / 2) & 1u, guard))) break;
+      fence_after();
+      const Aux& u = aux[r.slot];
+#pragma unroll 1
+      for (int c0 = 0; c0 < kSub; c0 += 32) {
+        float s[32], d[32];
+        tmem_ld32(s_at(wg) + lanes + c0, s);
+        tmem_ld32(dp_at(wg) + lanes + c0, d);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 lse = KV ? *reinterpret_cast<const float4*>(u.lse + c0 + c) : make_float4(lse_r, lse_r, lse_r, lse_r);
+          const float4 del = KV ? *reinterpret_cast<const float4*>(u.delta + c0 + c) : make_float4(delta_r, delta_r, delta_r, delta_r);
+          const float ls[4] = {lse.x, lse.y, lse.z, lse.w}, de[4] = {del.x, del.y, del.z, del.w};
+          float far[4] = {};
+          if (AXES) {
+#pragma unroll
+            for (int ax = 0; ax < 3; ++ax) {
+              const float4 k = *reinterpret_cast<const float4*>(u.pos[ax] + c0 + c);
+              far[0] += fabsf(pos[ax] - k.x);
+              far[1] += fabsf(pos[ax] - k.y);
+              far[2] += fabsf(pos[ax] - k.z);
+              far[3] += fabsf(pos[ax] - k.w);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float& v = s[c + e];
+            float slope = 1.0f;
+            if (CAP) {  // cap (1 - 2 q) with q = 1 / (1 + e^2y); derivative 4 q (1 - q)
+              const float q = rcp(1.0f + ex2(v * f.cap_in));
+              slope = 4.0f * q * (1.0f - q);
+              v = fmaf(-2.0f * f.cap2, q, f.cap2) - far[e];
+              v = ex2(v - ls[e]);
+            } else {
+              v = ex2(fmaf(v, f.c, -(AXES ? far[e] + ls[e] : ls[e])));
+            }
+            d[c + e] = v * (d[c + e] - de[e]);
+            if (CAP) d[c + e] *= slope;
+          }
+        }
+        if (cur.code == kMasked) {
+          const unsigned bad = u.bad[c0 / 32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            bool see = KV ? x < u.limit[c0 + c] : cur.n * kSub + c0 + c < limit;
+            if (a.doc_q) see = see && doc >= 0 && u.doc[c0 + c] == doc;
+            const float poison = (bad >> c) & 1u ? NAN : 0.0f;
+            s[c] = see ? s[c] + poison : 0.0f;
+            d[c] = see ? d[c] + poison : 0.0f;
+          }
+        }
+        uint32_t w[16];
+        if (KV) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) w[c] = pack2<T>(s[2 * c], s[2 * c + 1]);
+          tmem_st16(s_at(wg) + lanes + c0 / 2, w);
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c) w[c] = pack2<T>(d[2 * c], d[2 * c + 1]);
+        tmem_st16(dp_at(wg) + lanes + c0 / 2, w);
+      }
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(pfull + 8 * wg);
+    }
+    ok = ok && bar_wait_warp(accfull, 0, guard);
+    fence_after();
+    // keys resident: gv from the first warpgroup, gk from the second; queries:
+    // half of gq's channels each
+    const HeadsView& out = KV ? (wg == 0 ? a.gv : a.gk) : a.gq;
+    const uint32_t acc = KV && wg == 0 ? acc1 : acc2;
+    const float scale = KV && wg == 0 ? 1.0f : a.scale;
+    T* o = static_cast<T*>(out.p) + b * out.sb + (int64_t)xc * out.st + hr * out.sh;
+    for (int c = KV ? 0 : 32 * wg; c < a.D; c += KV ? 32 : 64) {
+      float v[32];
+      if (ok && n) {
+        tmem_ld32(acc + lanes + c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] *= scale;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 32; e += 8)
+        if (valid && c + e < a.D)
+          *reinterpret_cast<uint4*>(o + c + e) = make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]),
+                                                            pack2<T>(v[e + 4], v[e + 5]), pack2<T>(v[e + 6], v[e + 7]));
+      __syncwarp();
+    }
+  }
+  fence_before();
+  __syncwarp();
+  __syncthreads();
+  fence_after();
+  if (warp == 9) tmem_free(tmem, kTmemCols);
 }
 
-unsigned blocks(int64_t rows) { return (unsigned)((rows + kWarps - 1) / kWarps); }
+// delta = sum_d go o, 16 lanes per row.
+template <class T>
+__global__ void __launch_bounds__(256) k_attn_delta(const AttnArgs a) {
+  const int64_t row = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
+  if (row >= (int64_t)a.B * a.Hq * a.Sq) return;
+  // neighbouring rows are neighbouring heads of a token, as most layouts hold them
+  const int h = (int)(row % a.Hq), i = (int)(row / a.Hq % a.Sq), b = (int)(row / a.Hq / a.Sq), c = threadIdx.x % 16 * 8;
+  float sum = 0.0f;
+  if (c < a.D) {
+    const T* o = static_cast<const T*>(a.o.p) + b * a.o.sb + (int64_t)i * a.o.st + h * a.o.sh + c;
+    const T* g = static_cast<const T*>(a.go.p) + b * a.go.sb + (int64_t)i * a.go.st + h * a.go.sh + c;
+    const uint4 x = *reinterpret_cast<const uint4*>(o), y = *reinterpret_cast<const uint4*>(g);
+    const T *xe = reinterpret_cast<const T*>(&x), *ye = reinterpret_cast<const T*>(&y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = fmaf(to_f32<T>(xe[e]), to_f32<T>(ye[e]), sum);
+  }
+  const unsigned half = 0xffffu << (threadIdx.x & 16);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) sum += __shfl_xor_sync(half, sum, o);
+  if (threadIdx.x % 16 == 0) a.delta[((int64_t)b * a.Hq + h) * a.Sq + i] = sum;
+}
+
+template <class T, int AXES, bool CAP, bool KV>
+cudaError_t run(const CUtensorMap* m, const BwdArgs& f, cudaStream_t s) {
+  static std::atomic<unsigned long long> granted{0};
+  const size_t smem = 1024 + (size_t)f.panels * (2 * kPanel + 2 * kStages * kSubPanel);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(granted.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k_attn_bwd<T, AXES, CAP, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             1024 + 2 * (2 * kPanel + 2 * kStages * kSubPanel));
+    if (e != cudaSuccess) return e;
+    granted.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const int64_t tiles = ((KV ? f.a.Sk : f.a.Sq) + kTile - 1) / kTile;
+  note_launch_begin(KV ? "k_attn_bwd_kv" : "k_attn_bwd_q", s);
+  k_attn_bwd<T, AXES, CAP, KV><<<(unsigned)(tiles * f.a.B * (KV ? f.a.Hk : f.a.Hq)), kThreads, smem, s>>>(m[0], m[1], m[2], m[3], f);
+  note_launch_end(s);
+  return cudaGetLastError();
+}
+
+template <class T, bool KV>
+cudaError_t pick(const CUtensorMap* m, const BwdArgs& f, cudaStream_t s) {
+  if (f.a.axes) return f.a.cap > 0.0f ? run<T, 3, true, KV>(m, f, s) : run<T, 3, false, KV>(m, f, s);
+  return f.a.cap > 0.0f ? run<T, 0, true, KV>(m, f, s) : run<T, 0, false, KV>(m, f, s);
+}
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
-cudaError_t launch_attention_bwd(int dt, const AttnArgs& a, cudaStream_t s) {
-  if (a.Sq) {
-    note_launch_begin("k_attn_bwd_q", s);
-    FFDP_TOK_SWITCH16(dt, T, (k_attn_bwd_q<T><<<blocks((int64_t)a.B * a.Hq * a.Sq), kWarps * 32, 0, s>>>(a)));
+size_t attention_bwd_bytes(const AttnArgs& a) {
+  return round256((size_t)a.B * a.Hq * a.Sq * 4) + round256((size_t)a.B * ((a.Sq + kTile - 1) / kTile) * sizeof(DocRange)) +
+         round256((size_t)a.B * ((a.Sk + kTile - 1) / kTile) * sizeof(DocRange));
+}
+
+cudaError_t launch_attention_bwd(int dt, const AttnArgs& args, void* ws, cudaStream_t s) {
+  BwdArgs f{};
+  f.a = args;
+  AttnArgs& a = f.a;
+  char* w = static_cast<char*>(ws);
+  a.delta = reinterpret_cast<float*>(w);
+  w += round256((size_t)a.B * a.Hq * a.Sq * 4);
+  cudaError_t e = cudaSuccess;
+  if (a.doc_q) {
+    DocRange* dq = reinterpret_cast<DocRange*>(w);
+    DocRange* dk = reinterpret_cast<DocRange*>(w + round256((size_t)a.B * ((a.Sq + kTile - 1) / kTile) * sizeof(DocRange)));
+    e = launch_doc_ranges(a, dq, dk, s);
+    f.dq = dq;
+    f.dk = dk;
+  }
+  if (e == cudaSuccess) e = device_error_word(&f.error);
+  if (e != cudaSuccess) return e;
+  f.panels = (a.D + 63) / 64;
+  const uint32_t negate = a.scale < 0.0f ? 1u << 13 : 0u;  // of A
+  f.idesc_dp = mma_idesc(dt == 2, false, false, kTile, kSub);
+  f.idesc_s = f.idesc_dp | negate;
+  f.idesc_acc = mma_idesc(dt == 2, false, true, kTile, (a.D + 15) / 16 * 16);
+  f.c = fabsf(a.scale) * kLog2e;
+  if (a.cap > 0.0f) {
+    f.cap_in = 2.0f * kLog2e * fabsf(a.scale) / a.cap;
+    f.cap2 = a.cap * kLog2e;
+  }
+  const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
+  if (rows) {
+    note_launch_begin("k_attn_delta", s);
+    FFDP_TOK_SWITCH16(dt, T, (k_attn_delta<T><<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(a)));
     note_launch_end(s);
   }
-  if (a.Sk) {
-    note_launch_begin("k_attn_bwd_kv", s);
-    FFDP_TOK_SWITCH16(dt, T, (k_attn_bwd_kv<T><<<blocks((int64_t)a.B * a.Hk * a.Sk), kWarps * 32, 0, s>>>(a)));
-    note_launch_end(s);
+  // an empty side loads nothing: any valid address serves its maps
+  HeadsView q = a.q, k = a.k, v = a.v, go = a.go;
+  if (a.Sq == 0) q = go = a.k;
+  if (a.Sk == 0) k = v = a.q;
+  for (int kv = 1; kv >= 0; --kv) {
+    if ((kv ? a.Sk : a.Sq) == 0) continue;
+    CUtensorMap m[4];
+    const int tq = kv ? kSub : kTile, tk = kv ? kTile : kSub;
+    e = heads_map(&m[kv ? 2 : 0], dt, q, a.B, a.Sq, a.Hq, a.D, tq, 1);
+    if (e == cudaSuccess) e = heads_map(&m[kv ? 3 : 1], dt, go, a.B, a.Sq, a.Hq, a.D, tq, 1);
+    if (e == cudaSuccess) e = heads_map(&m[kv ? 0 : 2], dt, k, a.B, a.Sk, a.Hk, a.D, tk, 1);
+    if (e == cudaSuccess) e = heads_map(&m[kv ? 1 : 3], dt, v, a.B, a.Sk, a.Hk, a.D, tk, 1);
+    if (e != cudaSuccess) return e;
+    FFDP_TOK_SWITCH16(dt, T, { e = kv ? pick<T, true>(m, f, s) : pick<T, false>(m, f, s); });
+    if (e != cudaSuccess) return e;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 }  // namespace ffdp

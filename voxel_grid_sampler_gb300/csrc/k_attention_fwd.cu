@@ -42,7 +42,7 @@ struct FwdArgs {
 
 // Per key-tile slot: positions (per query tile, scaled by its head's slopes,
 // or raw when the tile's heads differ), documents, non-finite rows of V.
-struct Aux {
+struct alignas(16) Aux {
   float pos[2][3][kTile];
   int doc[kTile];
   unsigned bad[4];
@@ -89,8 +89,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int j0 = (int)((int64_t)f.nk * split / f.splits), j1 = (int)((int64_t)f.nk * (split + 1) / f.splits);
   for (int j = j0 + threadIdx.x; j < j1; j += kThreads)
-    codes[j - j0] = (uint8_t)(pair_code(a, prefix, b, i0[0], i1[0], j, f.dq, f.dk) |
-                              pair_code(a, prefix, b, i0[1], i1[1], j, f.dq, f.dk) << 2);
+    codes[j - j0] = (uint8_t)(pair_code(a, prefix, b, i0[0], i1[0], j * kTile, (j + 1) * kTile, f.dq, f.dk) |
+                              pair_code(a, prefix, b, i0[1], i1[1], j * kTile, (j + 1) * kTile, f.dq, f.dk) << 2);
   if (threadIdx.x == 0) {
     dead = 0;
     bar_init(qfull, 1);
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   #pragma unroll
           for (int i = 0; i < 4; ++i) {
             x.doc[i * 32 + lane] = doc[i];
-            const unsigned m = __ballot_sync(0xffffffffu, clear_bad_row<T>(sv + slot * tile_bytes, f.panels, i * 32 + lane));
+            const unsigned m = __ballot_sync(0xffffffffu, clear_bad_row<T>(sv + slot * tile_bytes, f.panels, kPanel, i * 32 + lane));
             if (lane == 0) x.bad[i] = m;
           }
           fence_async_smem();
