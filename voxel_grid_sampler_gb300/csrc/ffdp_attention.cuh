@@ -9,7 +9,7 @@ namespace ffdp {
 
 constexpr int kTile = 128;           // tokens per tile, queries and keys
 constexpr int kPanel = kTile * 128;  // bytes of 64 channels of a tile in shared memory
-constexpr int kMaxCodes = 4096;      // tile codes a CTA keeps; longer ranges are split
+constexpr int kMaxCodes = 2048;      // key tiles a work item lists; longer ranges are split
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -24,6 +24,70 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two floats in a register pair, for the instructions that work on both.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 split(f32x2 v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// -|v| of both: sign bits set, in place (taking the pair apart for scalar
+// operations costs two moves per pair).
+__device__ __forceinline__ f32x2 neg_abs2(f32x2 v) { return v | 0x8000000080000000ull; }
+
+// n / d for n < 2^31 by a multiplication (d >= 1).
+struct Divisor {
+  uint32_t mul;
+  int shift, d;
+};
+inline Divisor divisor(int d) {
+  Divisor r{0, 0, d};
+  while ((1ll << r.shift) < d) ++r.shift;
+  r.mul = (uint32_t)((((1ull << r.shift) - d) << 32) / d + 1);
+  return r;
+}
+__device__ __forceinline__ int div_by(int n, const Divisor& v) {
+  return (int)((__umulhi((uint32_t)n, v.mul) + (uint32_t)n) >> v.shift);
+}
+
+// Smallest and largest value of a warp.
+__device__ __forceinline__ float warp_min(float v) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 template <class T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   uint32_t d;
@@ -35,13 +99,18 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, f
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-// Whether either half of a packed pair is infinite or NaN.
-template <class T> __device__ __forceinline__ bool bad2(uint32_t u);
-template <> __device__ __forceinline__ bool bad2<__half>(uint32_t u) {
-  return (u & 0x7c00u) == 0x7c00u || (u & 0x7c000000u) == 0x7c000000u;
+// acc + 0 v of packed pairs: stays 0 over finite values, NaN from the first
+// infinity or NaN on.
+template <class T> __device__ __forceinline__ uint32_t zero_times(uint32_t v, uint32_t acc);
+template <> __device__ __forceinline__ uint32_t zero_times<__half>(uint32_t v, uint32_t acc) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0u), "r"(acc));
+  return d;
 }
-template <> __device__ __forceinline__ bool bad2<__nv_bfloat16>(uint32_t u) {
-  return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u;
+template <> __device__ __forceinline__ uint32_t zero_times<__nv_bfloat16>(uint32_t v, uint32_t acc) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0u), "r"(acc));
+  return d;
 }
 
 // Documents of a tile: range of the valid ids, whether any token is padding.
@@ -83,18 +152,24 @@ __device__ __forceinline__ int pair_code(const AttnArgs& a, int prefix, int b, i
 
 // A row of a [rows][64 channels per panel] tile in shared memory holds an
 // infinity or NaN: zero it (its products with masked weights must vanish) and
-// say so.
+// say so.  Lanes of a warp take neighbouring rows; each begins at another
+// 16-byte piece, so that eight lanes cover all banks.
 template <class T>
 __device__ __forceinline__ bool clear_bad_row(char* tile, int panels, int panel_bytes, int row) {
-  bool bad = false;
+  uint32_t acc[4] = {};
   for (int p = 0; p < panels; ++p) {
     const uint4* r = reinterpret_cast<const uint4*>(tile + p * panel_bytes + row * 128);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const uint4 u = r[c];
-      bad |= bad2<T>(u.x) || bad2<T>(u.y) || bad2<T>(u.z) || bad2<T>(u.w);
+      const uint4 u = r[c ^ (row & 7)];
+      acc[0] = zero_times<T>(u.x, acc[0]);
+      acc[1] = zero_times<T>(u.y, acc[1]);
+      acc[2] = zero_times<T>(u.z, acc[2]);
+      acc[3] = zero_times<T>(u.w, acc[3]);
     }
   }
+  // zeros of either sign, unless something was not finite
+  const bool bad = ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0;
   if (bad)
     for (int p = 0; p < panels; ++p) {
       uint4* r = reinterpret_cast<uint4*>(tile + p * panel_bytes + row * 128);

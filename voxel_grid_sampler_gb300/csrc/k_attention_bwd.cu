@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 3; ++x)
             pos[i][x] = x < a.axes && in ? pp[(int64_t)y * a.axes + x] * (a.slopes[h * a.axes + x] * kLog2e) : 0.0f;
         }
-        doc[i] = a.doc_q && masked && in ? (KV ? a.doc_q[b * a.doc_q_sb + y] : a.doc_k[b * a.doc_k_sb + y]) : -1;
+        doc[i] = a.doc_q && masked && in ? max(KV ? a.doc_q[b * a.doc_q_sb + y] : a.doc_k[b * a.doc_k_sb + y], -1) : -1;
       }
       if (!bar_wait_warp(tfull + 8 * r.slot, r.phase, guard)) break;
       Aux& x = aux[r.slot];
@@ -280,7 +280,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 3; ++i) raw_pos[i] = i < a.axes ? pp[(int64_t)xc * a.axes + i] : 0.0f;
     }
-    const int doc = a.doc_q ? (KV ? a.doc_k[b * a.doc_k_sb + xc] : a.doc_q[b * a.doc_q_sb + xc]) : 0;
+    int doc = a.doc_q ? (KV ? a.doc_k[b * a.doc_k_sb + xc] : a.doc_q[b * a.doc_q_sb + xc]) : 0;
+    if (doc < 0) doc = -2;  // padding: walked padding is -1
     const int limit = KV ? 0 : key_limit(a, prefix, xc);
     float lse_r = 0.0f, delta_r = 0.0f;
     if (!KV) {
@@ -344,14 +345,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (cur.code == kMasked) {
-          const unsigned bad = u.bad[c0 / 32];
+          if (KV && a.causal) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            bool see = KV ? x < u.limit[c0 + c] : cur.n * kSub + c0 + c < limit;
-            if (a.doc_q) see = see && doc >= 0 && u.doc[c0 + c] == doc;
-            const float poison = (bad >> c) & 1u ? NAN : 0.0f;
-            s[c] = see ? s[c] + poison : 0.0f;
-            d[c] = see ? d[c] + poison : 0.0f;
+            for (int c = 0; c < 32; c += 4) {
+              const int4 q = *reinterpret_cast<const int4*>(u.limit + c0 + c);
+              const int lim[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s[c + e] = x < lim[e] ? s[c + e] : 0.0f;
+                d[c + e] = x < lim[e] ? d[c + e] : 0.0f;
+              }
+            }
+          } else if (!KV) {
+            const int left = limit - cur.n * kSub - c0;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) d[c] = c < left ? d[c] : 0.0f;
+          }
+          if (a.doc_q) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              const int4 q = *reinterpret_cast<const int4*>(u.doc + c0 + c);
+              const int dc[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s[c + e] = doc == dc[e] ? s[c + e] : 0.0f;
+                d[c + e] = doc == dc[e] ? d[c + e] : 0.0f;
+              }
+            }
+          }
+          const unsigned bad = u.bad[c0 / 32];
+          if (bad) {  // a visible non-finite row makes this thread's results NaN
+            bool poison = false;
+#pragma unroll 1
+            for (int c = 0; c < 32; ++c) {
+              if (!((bad >> c) & 1u)) continue;
+              bool see = KV ? !a.causal || x < u.limit[c0 + c] : cur.n * kSub + c0 + c < limit;
+              if (a.doc_q) see = see && doc == u.doc[c0 + c];
+              poison |= see;
+            }
+            if (poison) s[0] = d[0] = NAN;
           }
         }
         uint32_t w[16];

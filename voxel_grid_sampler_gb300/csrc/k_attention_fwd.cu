@@ -1,15 +1,19 @@
 // k_attention_fwd.cu -- attention over volume tokens, forward.
 //
-// One CTA holds two tiles of 128 query rows that share their keys: the rows of
+// A work item is two tiles of 128 query rows that share their keys: the rows of
 // a tile are 128 tokens of one head, or, with few queries, the tokens of
 // several heads of one key head.  Per key tile: S = Q K^T on tcgen05 into TMEM;
-// a warpgroup per query tile (one row per thread) turns S into scores, keeps
-// the running maximum and sum, and writes P = 2^(score - maximum) back to TMEM
-// in 16 bits; O += P V on tcgen05.  The two tiles take turns on the tensor
-// cores and the arithmetic units.  Warps: 0-3 and 4-7 softmax of tiles 0 and
-// 1, 8 loads (TMA), 9 multiplies, 10 prepares the key tile's positions,
-// documents and non-finite rows.  Registers: 384 threads start with 168 each; the
-// softmax warps, which hold a row of 128 scores, take 208 and leave 88.
+// a warpgroup per query tile turns S into scores, keeps the running maximum and
+// sum of its rows, and writes P = 2^(score - maximum) back to TMEM in 16 bits;
+// O += P V on tcgen05.  One CTA per SM walks the items, so that the next item's
+// loads and first products run while the last one ends.  Warps: 0-3 and 4-7
+// softmax of tiles 0 and 1, 8 plans and loads (TMA), 9 and 11 issue the products
+// of tiles 0 and 1, 10 prepares the key tile's positions, documents and
+// non-finite rows.  The softmax arithmetic bounds it.  A softmax thread holds
+// four rows by 32 keys (a fragment) and not one row by 128: what depends on the
+// key (positions, documents) is read from shared memory four times less often.
+// 384 threads start with 168 registers each, the softmax warps take 208 and
+// leave 88.
 #include <atomic>
 
 #include "ffdp_attention.cuh"
@@ -32,6 +36,8 @@ struct FwdArgs {
   int rh, gb;
   int tiles, pairs; // query tiles and pairs of them per key head
   int splits, nk;   // splits of the key tiles, key tiles in all
+  int items, sms;
+  Divisor by_splits, by_pairs, by_hk, by_g, by_bgs, by_rh;  // bgs: B Hk splits
   int panels, stages;
   uint32_t idesc_s, idesc_o;
   float c;          // |scale| log2 e
@@ -40,13 +46,65 @@ struct FwdArgs {
   unsigned* error;
 };
 
-// Per key-tile slot: positions (per query tile, scaled by its head's slopes,
-// or raw when the tile's heads differ), documents, non-finite rows of V.
+// Per key-tile slot: the distance bias, documents, non-finite rows of V.
+// Positions are taken relative to the query tile's first row (differences of
+// near tokens stay exact) and scaled by its head's slopes.  Along an axis on
+// which no key of the tile lies between two queries of the query tile, |q - k|
+// is q - k or k - q for every pair: its key part goes into one constant per key
+// and its query part into one per row (`side`: +1 keys above, -1 below, 0
+// neither).  Tokens in raster order leave one or two axes per pair of tiles.
+// Tiles whose rows are of several heads hold raw positions.
 struct alignas(16) Aux {
   float pos[2][3][kTile];
+  float fold[2][kTile];
   int doc[kTile];
+  float side[2][4];
   unsigned bad[4];
 };
+
+// What a role knows of a work item.
+struct Item {
+  int b, g, split, j0, n;  // n: key tiles of the item's range, before skipping
+  int head[2], i0[2], i1[2];
+};
+
+template <bool PACKED>
+__device__ __forceinline__ Item item_of(const FwdArgs& f, int w) {
+  const AttnArgs& a = f.a;
+  Item x;
+  int pair, bg;
+  if (a.causal) {  // the longest rows first
+    pair = div_by(w, f.by_bgs);
+    w -= pair * f.by_bgs.d;
+    pair = f.pairs - 1 - pair;
+    bg = div_by(w, f.by_splits);
+    x.split = w - bg * f.splits;
+  } else {
+    const int rest = div_by(w, f.by_splits);
+    x.split = w - rest * f.splits;
+    bg = div_by(rest, f.by_pairs);
+    pair = rest - bg * f.pairs;
+  }
+  x.b = div_by(bg, f.by_hk);
+  x.g = bg - x.b * a.Hk;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int y = 2 * pair + t;
+    if (PACKED) {
+      x.head[t] = x.g * a.G + y * f.gb;
+      x.i0[t] = 0;
+      x.i1[t] = y < f.tiles ? a.Sq : 0;
+    } else {
+      const int q = div_by(y, f.by_g);
+      x.head[t] = x.g * a.G + y - q * a.G;
+      x.i0[t] = q * kTile;
+      x.i1[t] = y < f.tiles ? min(a.Sq, x.i0[t] + kTile) : x.i0[t];
+    }
+  }
+  x.j0 = f.splits == 1 ? 0 : div_by(f.nk * x.split, f.by_splits);
+  x.n = (f.splits == 1 ? f.nk : div_by(f.nk * (x.split + 1), f.by_splits)) - x.j0;
+  return x;
+}
 
 template <class T, int AXES, bool CAP, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -54,59 +112,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap mv, const FwdArgs f) {
   extern __shared__ char raw[];
   char* base = reinterpret_cast<char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t bars[1 + 5 * kMaxStages + 7];
-  __shared__ unsigned dead, tmem_slot;
-  __shared__ uint8_t codes[kMaxCodes];
+  __shared__ uint64_t bars[6 + 5 * kMaxStages + 9];
+  __shared__ volatile unsigned dead;
+  __shared__ unsigned tmem_slot;
+  // the plan of an item: its visible key tiles in order, index | code << 11
+  // (code: 2 bits per query tile), in two buffers
+  __shared__ uint16_t plan[2][kMaxCodes];
+  __shared__ int planned[2];
+  __shared__ float2 stats[2][kTile];  // per query tile and row: maximum, sum
+  __shared__ float rowpos[2][3][kTile];  // the rows' positions, as the keys' in Aux
+  __shared__ int rowlimit[2][kTile], rowdoc[2][kTile];
   __shared__ __align__(16) Aux aux[kMaxStages];
   const AttnArgs& a = f.a;
   const int NS = f.stages, tile_bytes = f.panels * kPanel;
   char *sq = base, *sk = sq + 2 * tile_bytes, *sv = sk + NS * tile_bytes;
-  const uint32_t qfull = smem_addr(bars), kfull = qfull + 8, kempty = kfull + 8 * kMaxStages, vfull = kempty + 8 * kMaxStages,
-                 vempty = vfull + 8 * kMaxStages, ready = vempty + 8 * kMaxStages, sfull = ready + 8 * kMaxStages,
-                 pfull = sfull + 16, pvdone = pfull + 16, drain = pvdone + 16;
+  const uint32_t qfull = smem_addr(bars), qempty = qfull + 8, pready = qempty + 8, pfree = pready + 16, kfull = pfree + 16,
+                 kempty = kfull + 8 * kMaxStages, vfull = kempty + 8 * kMaxStages, vempty = vfull + 8 * kMaxStages,
+                 ready = vempty + 8 * kMaxStages, sfull = ready + 8 * kMaxStages, sread = sfull + 16, pfull = sread + 16,
+                 pvdone = pfull + 16, drain = pvdone + 16;
   const Guard guard{&dead, f.error};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-
-  const int split = blockIdx.x % f.splits, rest = blockIdx.x / f.splits;
-  const int bg = rest / f.pairs, b = bg / a.Hk, g = bg - b * a.Hk;
-  int pair = rest - bg * f.pairs;
-  if (a.causal) pair = f.pairs - 1 - pair;  // the longest rows first
-  const int prefix = prefix_of(a, b);
-  // head and first token of this CTA's tiles
-  int head[2], i0[2], i1[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int x = 2 * pair + t;
-    if (PACKED) {
-      head[t] = g * a.G + x * f.gb;
-      i0[t] = 0;
-      i1[t] = x < f.tiles ? a.Sq : 0;
-    } else {
-      head[t] = g * a.G + x % a.G;
-      i0[t] = x / a.G * kTile;
-      i1[t] = x < f.tiles ? min(a.Sq, i0[t] + kTile) : i0[t];
-    }
-  }
-  const int j0 = (int)((int64_t)f.nk * split / f.splits), j1 = (int)((int64_t)f.nk * (split + 1) / f.splits);
-  for (int j = j0 + threadIdx.x; j < j1; j += kThreads)
-    codes[j - j0] = (uint8_t)(pair_code(a, prefix, b, i0[0], i1[0], j * kTile, (j + 1) * kTile, f.dq, f.dk) |
-                              pair_code(a, prefix, b, i0[1], i1[1], j * kTile, (j + 1) * kTile, f.dq, f.dk) << 2);
   if (threadIdx.x == 0) {
     dead = 0;
     bar_init(qfull, 1);
+    bar_init(qempty, 2);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(pready + 8 * i, 1);
+      bar_init(pfree + 8 * i, 11);
+    }
     for (int i = 0; i < kMaxStages; ++i) {
       bar_init(kfull + 8 * i, 1);
-      bar_init(kempty + 8 * i, 1);
+      bar_init(kempty + 8 * i, 2);
       bar_init(vfull + 8 * i, 1);
-      bar_init(vempty + 8 * i, 1);
+      bar_init(vempty + 8 * i, 2);
       bar_init(ready + 8 * i, 1);
     }
     for (int t = 0; t < 2; ++t) {
       bar_init(sfull + 8 * t, 1);
+      bar_init(sread + 8 * t, 4);
       bar_init(pfull + 8 * t, 4);
       bar_init(pvdone + 8 * t, 1);
     }
-    bar_init(drain, 1);
+    bar_init(drain, 2);
     bar_init_fence();
   }
   if (warp == 9) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
@@ -121,344 +168,603 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto s_at = [&](int t) { return tmem + t * 128; };
   auto o_at = [&](int t) { return tmem + 256 + t * o_cols; };
   auto p_at = [&](int t) { return own_p ? tmem + 384 + t * 64 : tmem + t * 128; };
-  const int n = j1 - j0;
-  int cur = 0;
-  auto next_tile = [&](int j) {  // first key tile at or after j that either query tile sees
-    while (j < n && codes[j] == 0) ++j;
-    return j;
-  };
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 8 && elect_one()) {
-      cur = next_tile(0);
-      if (cur < n) {
-        unsigned issued = 0;
-        const int rows = f.rh * f.gb;
-        const int valid = i1[1] > i0[1] ? 2 : 1;
-        bar_expect(qfull, valid * f.panels * rows * 128);
-        for (int t = 0; t < valid; ++t)
-          for (int p = 0; p < f.panels; ++p)
-            tma_load_4d(smem_addr(sq + t * tile_bytes + p * kPanel), &mq, p * 64, i0[t], head[t], b, qfull);
-        int slot = 0;
-        unsigned phase = 0;
-        for (; cur < n; cur = next_tile(cur + 1)) {
-          if (!bar_wait(kempty + 8 * slot, phase ^ 1u, guard)) break;
-          bar_expect(kfull + 8 * slot, tile_bytes);
-          for (int p = 0; p < f.panels; ++p)
-            tma_load_4d(smem_addr(sk + slot * tile_bytes + p * kPanel), &mk, p * 64, (j0 + cur) * kTile, g, b, kfull + 8 * slot);
-          const bool ok = bar_wait(vempty + 8 * slot, phase ^ 1u, guard);
-          if (!ok) {
-            bar_drain(kfull + 8 * slot, phase);
-            break;
+    if (warp == 8) {
+      unsigned qn = 0, k = 0, issued = 0;  // items with tiles, items, tiles loaded
+      int slot = 0;
+      unsigned phase = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; ok && w < f.items; w += gridDim.x, ++k) {
+        const Item x = item_of<PACKED>(f, w);
+        const int prefix = prefix_of(a, x.b), buf = k & 1;
+        if (!(ok = bar_wait_warp(pfree + 8 * buf, ((k >> 1) & 1u) ^ 1u, guard))) break;
+        int count = 0;
+        for (int j = 0; j < x.n; j += 32) {
+          int code = 0;
+          if (j + lane < x.n) {
+            const int y0 = (x.j0 + j + lane) * kTile;
+            code = pair_code(a, prefix, x.b, x.i0[0], x.i1[0], y0, y0 + kTile, f.dq, f.dk) |
+                   pair_code(a, prefix, x.b, x.i0[1], x.i1[1], y0, y0 + kTile, f.dq, f.dk) << 2;
           }
-          bar_expect(vfull + 8 * slot, tile_bytes);
-          for (int p = 0; p < f.panels; ++p)
-            tma_load_4d(smem_addr(sv + slot * tile_bytes + p * kPanel), &mv, p * 64, (j0 + cur) * kTile, g, b, vfull + 8 * slot);
-          ++issued;
-          if (++slot == NS) slot = 0, phase ^= 1u;
+          const unsigned seen = __ballot_sync(0xffffffffu, code != 0);
+          if (code) plan[buf][count + __popc(seen & ((1u << lane) - 1u))] = (uint16_t)((j + lane) | code << 11);
+          count += __popc(seen);
         }
-        bar_drain(qfull, 0);
+        if (lane == 0) planned[buf] = count;
+        __syncwarp();
+        if (lane == 0) bar_arrive(pready + 8 * buf);
+        if (count == 0) continue;
+        if (lane == 0) {
+          ok = bar_wait(qempty, (qn & 1u) ^ 1u, guard);
+          if (ok) {
+            const int valid = x.i1[1] > x.i0[1] ? 2 : 1;
+            bar_expect(qfull, valid * f.panels * f.rh * f.gb * 128);
+            for (int t = 0; t < valid; ++t)
+              for (int p = 0; p < f.panels; ++p)
+                tma_load_4d(smem_addr(sq + t * tile_bytes + p * kPanel), &mq, p * 64, x.i0[t], x.head[t], x.b, qfull);
+            ++qn;
+          }
+          for (int i = 0; ok && i < count; ++i) {
+            const int y = (x.j0 + (plan[buf][i] & 2047)) * kTile;
+            if (!(ok = bar_wait(kempty + 8 * slot, phase ^ 1u, guard))) break;
+            bar_expect(kfull + 8 * slot, tile_bytes);
+            for (int p = 0; p < f.panels; ++p)
+              tma_load_4d(smem_addr(sk + slot * tile_bytes + p * kPanel), &mk, p * 64, y, x.g, x.b, kfull + 8 * slot);
+            if (!(ok = bar_wait(vempty + 8 * slot, phase ^ 1u, guard))) {
+              bar_drain(kfull + 8 * slot, phase);
+              break;
+            }
+            bar_expect(vfull + 8 * slot, tile_bytes);
+            for (int p = 0; p < f.panels; ++p)
+              tma_load_4d(smem_addr(sv + slot * tile_bytes + p * kPanel), &mv, p * 64, y, x.g, x.b, vfull + 8 * slot);
+            ++issued;
+            if (++slot == NS) slot = 0, phase ^= 1u;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+      }
+      if (lane == 0) {
+        if (qn) bar_drain(qfull, (qn - 1) & 1u);
         for (unsigned i = issued > (unsigned)NS ? issued - NS : 0; i < issued; ++i) {
           bar_drain(kfull + 8 * (i % NS), (i / NS) & 1);
           bar_drain(vfull + 8 * (i % NS), (i / NS) & 1);
         }
       }
-    } else if (warp == 9 && elect_one()) {
-      const int ksteps = (a.D + 15) / 16;
-      int ks = 0, vs = 0;
-      unsigned kp = 0, vp = 0, done[2] = {0, 0};  // products P V issued per query tile
-      auto scores = [&](int t, int slot) {
-        for (int k = 0; k < ksteps; ++k) {
-          const uint32_t off = (k / 4) * kPanel + (k % 4) * 32;
-          mma_ss(s_at(t), smem_desc(smem_addr(sq + t * tile_bytes) + off, 16, 1024),
-                 smem_desc(smem_addr(sk + slot * tile_bytes) + off, 16, 1024), f.idesc_s, k > 0);
-        }
-        mma_commit(sfull + 8 * t);
+    } else if (warp != 10 && elect_one()) {
+      // The products of query tile t.  S of the next key tile is issued as soon
+      // as the last S was read (P apart) or its P consumed (P in S's place), P V
+      // as soon as P is written; `sc` walks ahead of `pv`.
+      const int t = warp == 9 ? 0 : 1;
+      struct Walk {
+        int w;        // work item
+        unsigned k;   // its number on this CTA
+        int i, n;     // position in its plan, plan's length (n < 0: not begun)
+        unsigned q;   // items with tiles so far
+        int slot;
+        unsigned phase;
       };
-      cur = next_tile(0);
-      bool ok = cur < n && bar_wait(qfull, 0, guard) && bar_wait(kfull, 0, guard);
-      if (ok) {
-        fence_after();
-        for (int t = 0; t < 2; ++t)
-          if ((codes[cur] >> (2 * t)) & 3) scores(t, 0);
-        mma_commit(kempty);
-        if (++ks == NS) ks = 0, kp ^= 1u;
-      }
-      while (ok) {
-        const int nxt = next_tile(cur + 1), code = codes[cur], ncode = nxt < n ? codes[nxt] : 0;
-        if (ncode && !(ok = bar_wait(kfull + 8 * ks, kp, guard))) break;
-        bool v_seen = false;
-        for (int t = 0; ok && t < 2; ++t) {
-          const bool now = (code >> (2 * t)) & 3, then = (ncode >> (2 * t)) & 3;
-          if (now) {
-            if (!(ok = bar_wait(pfull + 8 * t, done[t] & 1u, guard))) break;
-            fence_after();
-          }
-          if (own_p && then) scores(t, ks);
-          if (now) {
-            if (!v_seen) {
-              if (!(ok = bar_wait(ready + 8 * vs, vp, guard))) break;
-              fence_after();
-              v_seen = true;
+      Walk sc{(int)blockIdx.x, 0, 0, -1, 0, 0, 0}, pv = sc;
+      bool ok = true;
+      unsigned scored = 0, done = 0;  // products S and P V issued
+      bool started = false;           // O holds this item's sums
+      const uint32_t hi = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_v = (uint32_t)(smem_desc(0, kPanel, 1024) >> 32);
+      const uint32_t q_lo = (uint32_t)smem_desc(smem_addr(sq + t * tile_bytes), 16, 1024),
+                     k_lo = (uint32_t)smem_desc(smem_addr(sk), 16, 1024), v_lo = (uint32_t)smem_desc(smem_addr(sv), kPanel, 1024);
+      const uint32_t step = tile_bytes >> 4, s_addr = s_at(t), o_addr = o_at(t), p_addr = p_at(t);
+      const int ksteps = (a.D + 15) / 16;
+      // Makes the walk stand on a key tile: false at the end, where that tile
+      // would be past item `last`, or when a wait gave up.  `leave` gives the
+      // plans it passes back.
+      auto begin = [&](Walk& x, bool leave, unsigned last) {
+        while (x.n < 0 || x.i >= x.n) {
+          if (x.n >= 0) {
+            if (leave) {
+              bar_arrive(pfree + 8 * (x.k & 1));
+              started = false;
             }
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(o_at(t), p_at(t) + k * 8, smem_desc(smem_addr(sv + vs * tile_bytes) + k * 2048, kPanel, 1024), f.idesc_o,
-                     done[t] || k > 0);
-            ++done[t];
-            mma_commit(pvdone + 8 * t);
+            x.w += gridDim.x;
+            ++x.k;
+            x.n = -1;
           }
-          if (!own_p && then) {  // S takes P's place: after the product that reads P
-            if (done[t] && !(ok = bar_wait(pvdone + 8 * t, (done[t] - 1) & 1u, guard))) break;
-            scores(t, ks);
+          if (x.w >= f.items || x.k > last) return false;
+          if (!(ok = bar_wait(pready + 8 * (x.k & 1), (x.k >> 1) & 1u, guard))) return false;
+          x.n = planned[x.k & 1];
+          x.i = 0;
+          if (x.n) ++x.q;
+        }
+        return true;
+      };
+      auto advance = [&](Walk& x) {
+        ++x.i;
+        if (++x.slot == NS) x.slot = 0, x.phase ^= 1u;
+      };
+      auto scores = [&]() {  // S of the walk's tile; false: a wait gave up
+        const bool see = (plan[sc.k & 1][sc.i] >> (11 + 2 * t)) & 3;
+        if (sc.i == 0 && !(ok = bar_wait(qfull, (sc.q - 1) & 1u, guard))) return;
+        if (!(ok = bar_wait(kfull + 8 * sc.slot, sc.phase, guard))) return;
+        if (see) {
+          if (scored && !(ok = own_p ? bar_wait(sread + 8 * t, (scored - 1) & 1u, guard)
+                                     : bar_wait(pvdone + 8 * t, (scored - 1) & 1u, guard)))
+            return;
+          fence_after();
+          const uint32_t kb = k_lo + sc.slot * step;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            constexpr uint32_t kP = kPanel >> 4;
+            if (k < ksteps)
+              mma_ss(s_addr, q_lo + (k / 4) * kP + (k % 4) * 2, hi, kb + (k / 4) * kP + (k % 4) * 2, hi, f.idesc_s, k > 0);
           }
+          mma_commit(sfull + 8 * t);
+          ++scored;
+          mma_commit(kempty + 8 * sc.slot);
+        } else {
+          bar_arrive(kempty + 8 * sc.slot);
+        }
+        if (sc.i == sc.n - 1) mma_commit(qempty);
+        advance(sc);
+      };
+      int ahead = 0;  // tiles that `sc` is ahead; into the next item at most, whose plan does not wait for this one's end
+      while (ok && begin(pv, true, 0xffffffffu)) {
+        while (ok && ahead < (own_p ? 2 : 1) && begin(sc, false, pv.k + 1)) {
+          scores();
+          ++ahead;
         }
         if (!ok) break;
-        mma_commit(vempty + 8 * vs);
-        if (++vs == NS) vs = 0, vp ^= 1u;
-        if (ncode) {
-          mma_commit(kempty + 8 * ks);
-          if (++ks == NS) ks = 0, kp ^= 1u;
+        const bool see = (plan[pv.k & 1][pv.i] >> (11 + 2 * t)) & 3;
+        if (!(ok = bar_wait(ready + 8 * pv.slot, pv.phase, guard))) break;
+        if (see) {
+          if (!(ok = bar_wait(pfull + 8 * t, done & 1u, guard))) break;
+          fence_after();
+          const uint32_t vb = v_lo + pv.slot * step;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k) mma_ts(o_addr, p_addr + k * 8, vb + k * 128, hi_v, f.idesc_o, started || k > 0);
+          mma_commit(pvdone + 8 * t);
+          started = true;
+          ++done;
+          mma_commit(vempty + 8 * pv.slot);
+        } else {
+          bar_arrive(vempty + 8 * pv.slot);
         }
-        cur = nxt;
-        if (cur >= n) break;
+        advance(pv);
+        --ahead;
       }
       mma_commit(drain);
       bar_drain(drain, 0);
     } else if (warp == 10) {
       int slot = 0;
-      unsigned phase = 0;
-      float slope[2][3];
-      if (AXES) {
-  #pragma unroll
-        for (int t = 0; t < 2; ++t)
-  #pragma unroll
-          for (int x = 0; x < 3; ++x)
-            slope[t][x] = PACKED ? 1.0f : (x < a.axes && i1[t] > i0[t] ? a.slopes[head[t] * a.axes + x] * kLog2e : 0.0f);
-      }
-      for (cur = next_tile(0); cur < n; cur = next_tile(cur + 1)) {
-        const int code = codes[cur];
-        const bool masked = (code & 3) == kMasked || (code >> 2) == kMasked;
-        float pos[4][3];
-        int doc[4];
-  #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = (j0 + cur) * kTile + i * 32 + lane;
-          if (AXES) {
-  #pragma unroll
-            for (int x = 0; x < 3; ++x)
-              pos[i][x] = x < a.axes && j < a.Sk ? a.pos_k[b * a.pos_k_sb + (int64_t)j * a.axes + x] : 0.0f;
-          }
-          doc[i] = a.doc_k && masked && j < a.Sk ? a.doc_k[b * a.doc_k_sb + j] : -1;
-        }
-        if (!bar_wait_warp(vfull + 8 * slot, phase, guard)) break;
-        Aux& x = aux[slot];
-        if (AXES) {
-  #pragma unroll
-          for (int i = 0; i < 4; ++i)
-  #pragma unroll
-            for (int c = 0; c < 3; ++c) {
-              x.pos[0][c][i * 32 + lane] = pos[i][c] * slope[0][c];
-              if (!PACKED) x.pos[1][c][i * 32 + lane] = pos[i][c] * slope[1][c];
+      unsigned phase = 0, k = 0;
+      bool ok = true;
+      for (int w = blockIdx.x; ok && w < f.items; w += gridDim.x, ++k) {
+        const Item it = item_of<PACKED>(f, w);
+        float slope[2][3], origin[2][3], qlo[2][3], qhi[2][3];
+        if (AXES && !PACKED) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+              slope[t][x] = origin[t][x] = qlo[t][x] = qhi[t][x] = 0.0f;
+              if (x >= a.axes || it.i1[t] <= it.i0[t]) continue;
+              slope[t][x] = a.slopes[it.head[t] * a.axes + x] * kLog2e;
+              const float* p = a.pos_q + it.b * a.pos_q_sb + x;
+              origin[t][x] = p[(int64_t)it.i0[t] * a.axes];
+              float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float v = p[(int64_t)min(it.i0[t] + i * 32 + lane, it.i1[t] - 1) * a.axes];
+                lo = fminf(lo, v);
+                hi = fmaxf(hi, v);
+              }
+              qlo[t][x] = warp_min(lo);
+              qhi[t][x] = warp_max(hi);
             }
         }
-        if (masked) {
-  #pragma unroll
+        const int buf = k & 1;
+        if (!(ok = bar_wait_warp(pready + 8 * buf, (k >> 1) & 1u, guard))) break;
+        const int count = planned[buf];
+        for (int e = 0; e < count; ++e) {
+          const int code = plan[buf][e] >> 11, j1 = (it.j0 + (plan[buf][e] & 2047)) * kTile + lane;
+          const bool masked = (code & 3) == kMasked || (code >> 2) == kMasked;
+          float pos[4][3];
+          int doc[4];
+#pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x.doc[i * 32 + lane] = doc[i];
-            const unsigned m = __ballot_sync(0xffffffffu, clear_bad_row<T>(sv + slot * tile_bytes, f.panels, kPanel, i * 32 + lane));
-            if (lane == 0) x.bad[i] = m;
+            const int j = j1 + i * 32;
+            if (AXES) {
+#pragma unroll
+              for (int x = 0; x < 3; ++x)
+                pos[i][x] = x < a.axes ? a.pos_k[it.b * a.pos_k_sb + (int64_t)min(j, a.Sk - 1) * a.axes + x] : 0.0f;
+            }
+            doc[i] = a.doc_k && masked && j < a.Sk ? max(a.doc_k[it.b * a.doc_k_sb + j], -1) : -1;
           }
-          fence_async_smem();
+          if (!(ok = bar_wait_warp(vfull + 8 * slot, phase, guard))) break;
+          Aux& x = aux[slot];
+          if (AXES && PACKED) {
+  #pragma unroll
+            for (int i = 0; i < 4; ++i)
+  #pragma unroll
+              for (int c = 0; c < 3; ++c) x.pos[0][c][i * 32 + lane] = pos[i][c];
+          } else if (AXES) {
+            float lo[3], hi[3];
+  #pragma unroll
+            for (int c = 0; c < 3; ++c) {
+              lo[c] = warp_min(fminf(fminf(pos[0][c], pos[1][c]), fminf(pos[2][c], pos[3][c])));
+              hi[c] = warp_max(fmaxf(fmaxf(pos[0][c], pos[1][c]), fmaxf(pos[2][c], pos[3][c])));
+            }
+  #pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              float fold[4] = {};
+  #pragma unroll
+              for (int c = 0; c < 3; ++c) {
+                const float side = lo[c] >= qhi[t][c] ? 1.0f : (hi[c] <= qlo[t][c] ? -1.0f : 0.0f);
+  #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float k = (pos[i][c] - origin[t][c]) * slope[t][c];
+                  fold[i] = fmaf(-side, k, fold[i]);
+                  if (side == 0.0f) x.pos[t][c][i * 32 + lane] = k;
+                }
+                if (lane == 0) x.side[t][c] = side;
+              }
+  #pragma unroll
+              for (int i = 0; i < 4; ++i) x.fold[t][i * 32 + lane] = fold[i];
+            }
+          }
+          if (masked) {
+  #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x.doc[i * 32 + lane] = doc[i];
+              const unsigned m =
+                  __ballot_sync(0xffffffffu, clear_bad_row<T>(sv + slot * tile_bytes, f.panels, kPanel, i * 32 + lane));
+              if (lane == 0) x.bad[i] = m;
+            }
+            fence_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(ready + 8 * slot);
+          if (++slot == NS) slot = 0, phase ^= 1u;
         }
         __syncwarp();
-        if (lane == 0) bar_arrive(ready + 8 * slot);
-        if (++slot == NS) slot = 0, phase ^= 1u;
+        if (lane == 0) bar_arrive(pfree + 8 * buf);
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int t = warp / 4;
-    const int r = (warp % 4) * 32 + lane;  // row of the tile, lane of TMEM
     const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
-    int i, h;
-    bool valid;
-    if (PACKED) {
-      const int hl = r / f.rh;
-      i = r - hl * f.rh;
-      h = head[t] + hl;
-      valid = hl < f.gb && h < (g + 1) * a.G && i < i1[t];
-    } else {
-      i = i0[t] + r;
-      h = head[t];
-      valid = i < i1[t];
-    }
-    if (!valid) i = i0[t], h = g * a.G;
-    const int limit = key_limit(a, prefix, i);
-    const int doc_q = a.doc_q && i1[t] > i0[t] ? a.doc_q[b * a.doc_q_sb + i] : 0;
-    float pq[3], sl[3];
-    if (AXES) {
-#pragma unroll
-      for (int x = 0; x < 3; ++x) {
-        sl[x] = x < a.axes && i1[t] > i0[t] ? a.slopes[h * a.axes + x] * kLog2e : 0.0f;
-        pq[x] = x < a.axes && i1[t] > i0[t] ? a.pos_q[b * a.pos_q_sb + (int64_t)i * a.axes + x] : 0.0f;
-        if (!PACKED) pq[x] *= sl[x];
-      }
-    }
-    float m = -INFINITY, l = 0.0f;  // maximum (base-2 units) that P is relative to, sum of P
-    unsigned sp = 0, count = 0;
+    const int r0 = (warp % 4) * 32 + lane / 4;  // this thread's rows: r0 + 8 y, y < 4
+    const int cb = 2 * (lane % 4);              // its keys: 8 g + cb + {0, 1}, g < 16
     int slot = 0;
-    unsigned phase = 0;
+    unsigned phase = 0, k = 0, count = 0;       // items, key tiles of this query tile
     bool ok = true;
-    for (cur = next_tile(0); cur < n; cur = next_tile(cur + 1)) {
-      const int code = (codes[cur] >> (2 * t)) & 3;
-      if (code) {
-        if (AXES || code == kMasked) {
-          if (!(ok = bar_wait_warp(ready + 8 * slot, phase, guard))) break;
+    for (int w = blockIdx.x; ok && w < f.items; w += gridDim.x, ++k) {
+      const Item it = item_of<PACKED>(f, w);
+      const int b = it.b, i0 = t ? it.i0[1] : it.i0[0], i1 = t ? it.i1[1] : it.i1[0], head = t ? it.head[1] : it.head[0];
+      const bool live = i1 > i0;
+      // token and head of a row of the tile; false: no such row
+      auto place = [&](int r, int* i, int* h) {
+        bool valid;
+        if (PACKED) {
+          const int hl = div_by(r, f.by_rh);
+          *i = r - hl * f.rh;
+          *h = head + hl;
+          valid = live && hl < f.gb && *h < (it.g + 1) * a.G && *i < i1;
+        } else {
+          *i = i0 + r;
+          *h = head;
+          valid = *i < i1;
         }
-        const Aux& x = aux[slot];
-        if (!(ok = bar_wait_warp(sfull + 8 * t, sp, guard))) break;
-        sp ^= 1u;
-        fence_after();
-        float s[kTile];
-#pragma unroll
-        for (int c = 0; c < kTile; c += 32) tmem_ld32(s_at(t) + lanes + c, s + c);
-        tmem_wait_ld();
-        if (CAP) {
-          // cap tanh(y) = cap - 2 cap / (1 + e^2y): two special-function
-          // operations with an error of 1e-7 cap, and right at infinities
-#pragma unroll
-          for (int c = 0; c < kTile; ++c) s[c] = fmaf(-2.0f * f.cap2, rcp(1.0f + ex2(s[c] * f.cap_in)), f.cap2);
-        } else if (AXES) {
-#pragma unroll
-          for (int c = 0; c < kTile; ++c) s[c] *= f.c;
-        }
+        if (!valid) *i = live ? i0 : 0, *h = it.g * a.G;
+        return valid;
+      };
+      float sl[PACKED ? 4 : 1][3];  // rows of several heads: each row's slopes
+      {
+        const int r = (warp % 4) * 32 + lane;
+        int i, h;
+        place(r, &i, &h);
+        __syncwarp();
+        rowlimit[t][r] = key_limit(a, prefix_of(a, b), i);
+        const int d = a.doc_q ? a.doc_q[b * a.doc_q_sb + i] : 0;
+        rowdoc[t][r] = d < 0 ? -2 : d;  // padded keys are -1: equal to no query
         if (AXES) {
+          const float* p = a.pos_q + b * a.pos_q_sb;
 #pragma unroll
-          for (int ax = 0; ax < 3; ++ax) {
-            const float4* kp = reinterpret_cast<const float4*>(x.pos[PACKED ? 0 : t][ax]);
+          for (int x = 0; x < 3; ++x) {
+            float v = 0.0f;
+            if (x < a.axes) {
+              v = p[(int64_t)i * a.axes + x];
+              if (!PACKED) v = (v - p[(int64_t)(live ? i0 : 0) * a.axes + x]) * (a.slopes[min(head, a.Hq - 1) * a.axes + x] * kLog2e);
+            }
+            rowpos[t][x][r] = v;
+          }
+        }
+        if (AXES && PACKED) {
 #pragma unroll
-            for (int c = 0; c < kTile; c += 4) {
-              const float4 k = kp[c / 4];
-              if (PACKED) {
-                s[c] = fmaf(-sl[ax], fabsf(pq[ax] - k.x), s[c]);
-                s[c + 1] = fmaf(-sl[ax], fabsf(pq[ax] - k.y), s[c + 1]);
-                s[c + 2] = fmaf(-sl[ax], fabsf(pq[ax] - k.z), s[c + 2]);
-                s[c + 3] = fmaf(-sl[ax], fabsf(pq[ax] - k.w), s[c + 3]);
-              } else {
-                s[c] -= fabsf(pq[ax] - k.x);
-                s[c + 1] -= fabsf(pq[ax] - k.y);
-                s[c + 2] -= fabsf(pq[ax] - k.z);
-                s[c + 3] -= fabsf(pq[ax] - k.w);
+          for (int y = 0; y < 4; ++y) {
+            place(r0 + 8 * y, &i, &h);
+#pragma unroll
+            for (int x = 0; x < 3; ++x) sl[PACKED ? y : 0][x] = x < a.axes ? a.slopes[h * a.axes + x] * kLog2e : 0.0f;
+          }
+        }
+        __syncwarp();
+      }
+      // maximum (base-2 units) that P is relative to; this thread's part of the sum of P
+      float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, l[4] = {};
+      bool first = true;
+      const int buf = k & 1;
+      if (!(ok = bar_wait_warp(pready + 8 * buf, (k >> 1) & 1u, guard))) break;
+      const int tiles = planned[buf];
+      for (int e = 0; e < tiles; ++e) {
+        const int entry = plan[buf][e], code = (entry >> (11 + 2 * t)) & 3;
+        if (code) {
+          if (AXES || code == kMasked) {
+            if (!(ok = bar_wait_warp(ready + 8 * slot, phase, guard))) break;
+          }
+          const Aux& x = aux[slot];
+          if (!(ok = bar_wait_warp(sfull + 8 * t, count & 1u, guard))) break;
+          fence_after();
+          f32x2 v[4][16];  // rows by pairs of keys
+          {
+            float s[128];
+            tmem_ld_frag16(s_at(t) + lanes, s);
+            tmem_ld_frag16(s_at(t) + lanes + (16u << 16), s + 64);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int g = 0; g < 16; ++g) {
+                const int at = (y / 2) * 64 + 4 * g + (y % 2) * 2;
+                v[y][g] = pair(s[at], s[at + 1]);
+              }
+          }
+          if (own_p) {  // the next S may be computed meanwhile
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(sread + 8 * t);
+          }
+          if (CAP) {
+            // cap tanh(y) = cap - 2 cap / (1 + e^2y): two special-function
+            // operations with an error of 1e-7 cap, and right at infinities
+            const f32x2 in = pair(f.cap_in, f.cap_in), out = pair(-2.0f * f.cap2, -2.0f * f.cap2), cap = pair(f.cap2, f.cap2);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int g = 0; g < 16; ++g) {
+                const float2 z = split(mul2(v[y][g], in));
+                v[y][g] = fma2(out, pair(rcp(1.0f + ex2(z.x)), rcp(1.0f + ex2(z.y))), cap);
+              }
+          }
+          float shift[4] = {};  // of whole rows
+          const float sc = CAP ? 1.0f : f.c;
+          if (AXES && PACKED) {
+#pragma unroll 1
+            for (int ax = 0; ax < 3; ++ax) {
+              const float* kp = x.pos[0][ax] + cb;
+              float p[4], q[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                p[y] = rowpos[t][ax][r0 + 8 * y];
+                q[y] = ax == 0 ? sl[PACKED ? y : 0][0] : (ax == 1 ? sl[PACKED ? y : 0][1] : sl[PACKED ? y : 0][2]);
+              }
+#pragma unroll
+              for (int g = 0; g < 16; ++g) {
+                const float2 kk = *reinterpret_cast<const float2*>(kp + 8 * g);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  float2 z = split(v[y][g]);
+                  if (ax == 0) z.x *= sc, z.y *= sc;
+                  v[y][g] = pair(fmaf(-q[y], fabsf(p[y] - kk.x), z.x), fmaf(-q[y], fabsf(p[y] - kk.y), z.y));
+                }
+              }
+            }
+          } else if (AXES) {
+            const float* kf = x.fold[t] + cb;
+            const f32x2 sc2 = pair(sc, sc);
+#pragma unroll
+            for (int g = 0; g < 16; ++g) {
+              const f32x2 kk = *reinterpret_cast<const f32x2*>(kf + 8 * g);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) v[y][g] = fma2(v[y][g], sc2, kk);
+            }
+#pragma unroll 1
+            for (int ax = 0; ax < 3; ++ax) {
+              const float side = x.side[t][ax];
+              f32x2 np[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float p = rowpos[t][ax][r0 + 8 * y];
+                shift[y] = fmaf(side, p, shift[y]);
+                np[y] = pair(-p, -p);
+              }
+              if (side != 0.0f) continue;
+              const float* kp = x.pos[t][ax] + cb;
+#pragma unroll
+              for (int g = 0; g < 16; ++g) {
+                const f32x2 kk = *reinterpret_cast<const f32x2*>(kp + 8 * g);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  v[y][g] = add2(v[y][g], neg_abs2(add2(kk, np[y])));
+                }
               }
             }
           }
-        }
-        const float c2 = CAP || AXES ? 1.0f : f.c;
-        if (code == kMasked) {
-          const int left = limit - (j0 + cur) * kTile;  // keys of this tile before the limit
+          const float c2 = CAP || AXES ? 1.0f : f.c;
+          if (code == kMasked) {
+            const int key0 = (it.j0 + (entry & 2047)) * kTile;
+            if (key0 + kTile > a.Sk || a.causal) {
 #pragma unroll
-          for (int c = 0; c < kTile; ++c) s[c] = c < left ? s[c] : -INFINITY;
-          if (a.doc_q) {
-            const int4* kd = reinterpret_cast<const int4*>(x.doc);
+              for (int y = 0; y < 4; ++y) {
+                const int left = rowlimit[t][r0 + 8 * y] - key0 - cb;  // keys before the limit, from this thread's first on
 #pragma unroll
-            for (int c = 0; c < kTile; c += 4) {
-              const int4 d = kd[c / 4];
-              s[c] = d.x == doc_q && doc_q >= 0 ? s[c] : -INFINITY;
-              s[c + 1] = d.y == doc_q && doc_q >= 0 ? s[c + 1] : -INFINITY;
-              s[c + 2] = d.z == doc_q && doc_q >= 0 ? s[c + 2] : -INFINITY;
-              s[c + 3] = d.w == doc_q && doc_q >= 0 ? s[c + 3] : -INFINITY;
+                for (int g = 0; g < 16; ++g) {
+                  const float2 z = split(v[y][g]);
+                  v[y][g] = pair(8 * g < left ? z.x : -INFINITY, 8 * g + 1 < left ? z.y : -INFINITY);
+                }
+              }
+            }
+            if (a.doc_q) {
+              int dq[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) dq[y] = rowdoc[t][r0 + 8 * y];
+#pragma unroll
+              for (int g = 0; g < 16; ++g) {
+                const int2 d = *reinterpret_cast<const int2*>(x.doc + 8 * g + cb);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  const float2 z = split(v[y][g]);
+                  v[y][g] = pair(d.x == dq[y] ? z.x : -INFINITY, d.y == dq[y] ? z.y : -INFINITY);
+                }
+              }
+            }
+            if (x.bad[0] | x.bad[1] | x.bad[2] | x.bad[3]) {  // a visible non-finite value makes the row NaN
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                bool poison = false;
+                const int limit = rowlimit[t][r0 + 8 * y], dq = rowdoc[t][r0 + 8 * y];
+#pragma unroll 1
+                for (int c = 0; c < kTile; ++c)
+                  if ((x.bad[c / 32] >> (c % 32)) & 1u) poison |= key0 + c < limit && (!a.doc_q || x.doc[c] == dq);
+                if (poison) v[y][0] = pair(NAN, NAN);
+              }
             }
           }
-          if (x.bad[0] | x.bad[1] | x.bad[2] | x.bad[3]) {  // a visible non-finite value makes the row NaN
+          bool grow[4], any = false;
+          float top[4];
 #pragma unroll
-            for (int c = 0; c < kTile; ++c)
-              if ((x.bad[c / 32] >> (c % 32)) & 1u) s[c] = s[c] == -INFINITY ? s[c] : NAN;
+          for (int y = 0; y < 4; ++y) {
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int g = 0; g < 16; ++g) {
+              const float2 z = split(v[y][g]);
+              mx[g % 2] = max3(mx[g % 2], z.x, z.y);
+            }
+            top[y] = fmaxf(mx[0], mx[1]);
           }
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int c = 4; c < kTile; ++c) mx[c % 4] = fmaxf(mx[c % 4], s[c]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
-        // own columns for P, or a rescaling of O: the last product must be done
-        const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
-        const bool rescale = __any_sync(0xffffffffu, grow);
-        if (count && (own_p || rescale)) {
-          if (!(ok = bar_wait_warp(pvdone + 8 * t, (count - 1) & 1u, guard))) break;
-          fence_after();
-        }
-        if (rescale) {
-          const float mn = grow ? top : m, w = grow ? ex2(m - mn) : 1.0f;  // 2^-inf = 0: no row before
-          m = mn;
-          l *= w;
-          if (count) {
-            for (int c = 0; c < a.D; c += 32) {
-              float o[32];
-              tmem_ld32(o_at(t) + lanes + c, o);
-              tmem_wait_ld();
+          for (int y = 0; y < 4; ++y) top[y] = fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 1));
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= w;
-              tmem_st32(o_at(t) + lanes + c, o);
+          for (int y = 0; y < 4; ++y) top[y] = fmaf(fmaxf(top[y], __shfl_xor_sync(0xffffffffu, top[y], 2)), c2, shift[y]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            grow[y] = top[y] > m[y] + kRescale || (m[y] == -INFINITY && top[y] > m[y]);
+            any |= grow[y];
+          }
+          const bool rescale = __any_sync(0xffffffffu, any);
+          // own columns for P, or a rescaling of O: the last product must be done
+          if (count && (own_p || (rescale && !first))) {
+            if (!(ok = bar_wait_warp(pvdone + 8 * t, (count - 1) & 1u, guard))) break;
+            fence_after();
+          }
+          if (rescale) {
+            float wt[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float mn = grow[y] ? top[y] : m[y];
+              wt[y] = grow[y] ? ex2(m[y] - mn) : 1.0f;  // 2^-inf = 0: no row before
+              m[y] = mn;
+              l[y] *= wt[y];
+            }
+            if (!first) {
+#pragma unroll 1
+              for (int c = 0; c < a.D; c += 16) {
+                float o[16];
+                tmem_ld_frag2(o_at(t) + lanes + c, o);
+                tmem_ld_frag2(o_at(t) + lanes + (16u << 16) + c, o + 8);
+                tmem_wait_ld();
+#pragma unroll
+                for (int z = 0; z < 16; ++z) o[z] *= wt[z / 8 * 2 + z / 2 % 2];
+                tmem_st_frag2(o_at(t) + lanes + c, o);
+                tmem_st_frag2(o_at(t) + lanes + (16u << 16) + c, o + 8);
+              }
             }
           }
-        }
-        const float mm = m == -INFINITY ? 0.0f : m;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const f32x2 c22 = pair(c2, c2);
+          f32x2 mm[4], sum[4];
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          uint32_t u[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float p0 = ex2(fmaf(s[c + e], c2, -mm)), p1 = ex2(fmaf(s[c + e + 1], c2, -mm));
-            sum[e % 4] += p0;
-            sum[e % 4 + 1] += p1;
-            u[e / 2] = pack2<T>(p0, p1);
+          for (int y = 0; y < 4; ++y) {
+            const float z = shift[y] - (m[y] == -INFINITY ? 0.0f : m[y]);
+            mm[y] = pair(z, z);
+            sum[y] = 0ull;
           }
-          tmem_st16(p_at(t) + lanes + c / 2, u);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {  // 16 lanes by 64 keys
+            uint32_t u[16];
+            const int y0 = q / 2 * 2;
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const f32x2 z = v[y0 + y][q % 2 * 8 + g];
+                const float2 d = split(CAP || AXES ? add2(z, mm[y0 + y]) : fma2(z, c22, mm[y0 + y]));
+                const float p0 = ex2(d.x), p1 = ex2(d.y);
+                sum[y0 + y] = add2(sum[y0 + y], pair(p0, p1));
+                u[2 * g + y] = pack2<T>(p0, p1);
+              }
+            tmem_st_packed8(p_at(t) + lanes + ((uint32_t)(q / 2 * 16) << 16) + q % 2 * 32, u);
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2 z = split(sum[y]);
+            l[y] += z.x + z.y;
+          }
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(pfull + 8 * t);
+          ++count;
+          first = false;
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(pfull + 8 * t);
-        ++count;
+        if (++slot == NS) slot = 0, phase ^= 1u;
       }
-      if (++slot == NS) slot = 0, phase ^= 1u;
-    }
-    // results: o = O / l, lse; of a split, both in 32 bits to the workspace
-    if (ok && count) ok = bar_wait_warp(pvdone + 8 * t, (count - 1) & 1u, guard);
-    fence_after();
-    if (i1[t] > i0[t]) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l, lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+      __syncwarp();
+      if (lane == 0) bar_arrive(pfree + 8 * buf);
+      if (!ok || !live) continue;
+      // results, one row per thread: o = O / l, lse; of a split, both in 32 bits
+      // to the workspace
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 1);
+        l[y] += __shfl_xor_sync(0xffffffffu, l[y], 2);
+        if (lane % 4 == 0) stats[t][r0 + 8 * y] = make_float2(m[y], l[y]);
+      }
+      __syncwarp();
+      if (!first) ok = bar_wait_warp(pvdone + 8 * t, (count - 1) & 1u, guard);
+      fence_after();
+      const int r = (warp % 4) * 32 + lane;
+      const float2 st = stats[t][r];
+      int i, h;
+      const bool valid = place(r, &i, &h);
+      const float inv = st.y == 0.0f ? 0.0f : 1.0f / st.y, lse2 = st.y == 0.0f ? -INFINITY : st.x + __log2f(st.y);
       const int64_t row = ((int64_t)b * a.Hq + h) * a.Sq + i, rows = (int64_t)a.B * a.Hq * a.Sq;
       if (valid) {
         if (f.splits > 1)
-          f.part[rows * a.D * f.splits + split * rows + row] = lse2;
+          f.part[rows * a.D * f.splits + it.split * rows + row] = lse2;
         else if (a.lse)
           a.lse[row] = lse2 * kLn2;
       }
+#pragma unroll 1
       for (int c = 0; c < a.D; c += 32) {
         float o[32];
-        if (ok && count) {
+        if (ok && !first) {
           tmem_ld32(o_at(t) + lanes + c, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = l == 0.0f ? 0.0f : o[e] * inv;
+          for (int z = 0; z < 32; ++z) o[z] = st.y == 0.0f ? 0.0f : o[z] * inv;
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+          for (int z = 0; z < 32; ++z) o[z] = 0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          if (!valid || c + e >= a.D) continue;
+        for (int z = 0; z < 32; z += 8) {
+          if (!valid || c + z >= a.D) continue;
           if (f.splits > 1) {
-            float* p = f.part + (split * rows + row) * a.D + c + e;
-            *reinterpret_cast<float4*>(p) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            *reinterpret_cast<float4*>(p + 4) = make_float4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
+            float* p = f.part + (it.split * rows + row) * a.D + c + z;
+            *reinterpret_cast<float4*>(p) = make_float4(o[z], o[z + 1], o[z + 2], o[z + 3]);
+            *reinterpret_cast<float4*>(p + 4) = make_float4(o[z + 4], o[z + 5], o[z + 6], o[z + 7]);
           } else {
-            T* p = static_cast<T*>(a.o.p) + b * a.o.sb + (int64_t)i * a.o.st + h * a.o.sh + c + e;
-            *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
-                                                      pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
+            T* p = static_cast<T*>(a.o.p) + b * a.o.sb + (int64_t)i * a.o.st + h * a.o.sh + c + z;
+            *reinterpret_cast<uint4*>(p) = make_uint4(pack2<T>(o[z], o[z + 1]), pack2<T>(o[z + 2], o[z + 3]),
+                                                      pack2<T>(o[z + 4], o[z + 5]), pack2<T>(o[z + 6], o[z + 7]));
           }
         }
         __syncwarp();
@@ -550,7 +856,7 @@ cudaError_t run(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap&
     if (e != cudaSuccess) return e;
     granted.fetch_or(bit, std::memory_order_relaxed);
   }
-  const unsigned grid = (unsigned)((int64_t)f.a.B * f.a.Hk * f.pairs * f.splits);
+  const int grid = f.items < f.sms ? f.items : f.sms;
   note_launch_begin("k_attn_fwd", s);
   k_attn_fwd<T, AXES, CAP, PACKED><<<grid, kThreads, smem, s>>>(mq, mk, mv, f);
   note_launch_end(s);
@@ -636,12 +942,20 @@ cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, int sms, void* ws, c
   f.tiles = p.tiles;
   f.pairs = p.pairs;
   f.splits = p.splits;
+  f.items = a.B * a.Hk * p.pairs * p.splits;
+  f.sms = sms;
+  f.by_splits = divisor(p.splits);
+  f.by_pairs = divisor(p.pairs);
+  f.by_hk = divisor(a.Hk);
+  f.by_g = divisor(a.G);
+  f.by_bgs = divisor(a.B * a.Hk * p.splits);
+  f.by_rh = divisor(p.rh);
   f.nk = p.nk;
   f.panels = (a.D + 63) / 64;
   f.stages = f.panels == 1 ? 4 : 2;
   f.idesc_s = tc::mma_idesc(dt == 2, false, false, kTile, kTile) | (a.scale < 0.0f ? 1u << 13 : 0u);  // negate A
   f.idesc_o = tc::mma_idesc(dt == 2, false, true, kTile, (a.D + 15) / 16 * 16);
-  f.c = fabsf(a.scale) * kLog2e;
+  f.c = fmaxf(fabsf(a.scale) * kLog2e, 1e-37f);  // not zero: a masked -inf stays one
   if (a.cap > 0.0f) {
     f.cap_in = 2.0f * kLog2e * fabsf(a.scale) / a.cap;
     f.cap2 = a.cap * kLog2e;
