@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -463,7 +464,44 @@ def ffdp_sobolev_adam_step(u, g, m1, m2, params: ffdp_sobolev_adam_params, u_out
 # library takes (last axis contiguous); matrices are (rows, columns) with
 # contiguous rows that may be padded.  Outputs default to contiguous tensors
 # (matrices: rows padded to 16 bytes).
+#
+# The smallest calls last about as long as their marshalling, so the argument
+# structs are packed with struct (ctypes.Structure costs about 1 us each) and go
+# through a second handle of the library that takes them as plain addresses.
 _DTYPES = {torch.float32: FFDP_F32, torch.float16: FFDP_F16, torch.bfloat16: FFDP_BF16}
+_ROPE_TENSOR = struct.Struct("8qi4x").pack      # ffdp_rope_tensor
+_ROPE_PARAMS = struct.Struct("2q6i").pack       # ffdp_rope_params
+_HEADS = struct.Struct("4q").pack               # ffdp_heads
+_ATTENTION_PARAMS = struct.Struct("3q3i2fi").pack
+_ATTENTION_BIAS = struct.Struct("5qi4x5q").pack
+_LINEAR_PARAMS = struct.Struct("3qi4x").pack
+_fast_lib = None
+
+
+def _fast() -> ctypes.CDLL:
+    global _fast_lib
+    if _fast_lib is None:
+        lib()
+        L = ctypes.CDLL(LIB_PATH)
+        i, i64, sz = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+        for f in (L.ffdp_rope_fwd, L.ffdp_rope_bwd):
+            f.argtypes = [_vp, i, i, _vp, _vp, i64, _vp, _vp]
+        L.ffdp_attention_fwd.argtypes = [_vp] * 5 + [i, _vp, _vp, _vp, sz, _vp]
+        L.ffdp_attention_bwd.argtypes = [_vp] * 9 + [i, _vp, _vp, _vp, sz, _vp]
+        L.ffdp_attention_workspace_bytes.argtypes = [_vp, i]
+        L.ffdp_attention_workspace_bytes.restype = sz
+        L.ffdp_linear_fwd.argtypes = [_vp, i64, _vp, i64, _vp, _vp, i64, _vp, i64, _vp, i64, i, _vp, _vp, sz, _vp]
+        L.ffdp_linear_bwd.argtypes = [_vp, i64, _vp, i64, _vp, i64, _vp, i64, _vp, i64, _vp, i64, _vp, i, _vp, _vp, sz, _vp]
+        L.ffdp_linear_workspace_bytes.argtypes = [_vp, i]
+        L.ffdp_linear_workspace_bytes.restype = sz
+        _fast_lib = L
+    return _fast_lib
+
+
+def _stream_of(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _tok(t, name, like=None, shape=None):
@@ -475,56 +513,64 @@ def _tok(t, name, like=None, shape=None):
         raise FfdpError(1, "%s must have the type and device of the first tensor" % name)
     if shape is not None and t.shape != shape:
         raise FfdpError(1, "%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.dim() > 1 and t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.stride()[-1] != 1 and t.shape[-1] > 1:
         raise FfdpError(1, "%s must have a contiguous last axis" % name)
     return t
 
 
-def _heads(t) -> ffdp_heads:
+def _tok4(t, name, like=None, shape=None):
+    if not isinstance(t, torch.Tensor) or t.dim() != 4:
+        raise FfdpError(1, "%s must be (batch, tokens, heads, head_dim)" % name)
+    return _tok(t, name, like, shape)
+
+
+def _heads(t) -> bytes:
     s = t.stride()
-    return ffdp_heads(t.data_ptr(), s[0], s[1], s[2])
+    return _HEADS(t.data_ptr(), s[0], s[1], s[2])
 
 
-def _const(t, name, dtype, device, tail):
-    """A constant array of shape tail, or (batch,) + tail: its pointer and batch stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device or t.dtype != dtype:
+def _const(t, name, dtype, device, tail, B=1):
+    """A constant array of shape tail, or (B,) + tail: its pointer and batch stride."""
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype:
         raise FfdpError(1, "%s must be a %s CUDA tensor on the tensors' device" % (name, dtype))
-    if t.shape[-len(tail):] != tail or t.dim() not in (len(tail), len(tail) + 1):
-        raise FfdpError(1, "%s must have shape %s, with or without a batch axis, got %s" % (name, tail, tuple(t.shape)))
-    inner = t[0] if t.dim() > len(tail) and t.shape[0] else t
-    if not inner.is_contiguous():
+    shape = t.shape
+    if shape == tail:
+        if not t.is_contiguous():
+            raise FfdpError(1, "%s must be contiguous" % name)
+        return t.data_ptr(), 0
+    if len(shape) != len(tail) + 1 or shape[1:] != tail or shape[0] != B:
+        raise FfdpError(1, "%s must have shape %s, with or without a batch axis of %d, got %s" % (name, tuple(tail), B, tuple(shape)))
+    if B and not t[0].is_contiguous():
         raise FfdpError(1, "%s must be contiguous within the batch" % name)
-    return t.data_ptr(), t.stride(0) if t.dim() > len(tail) and t.shape[0] > 1 else 0
+    return t.data_ptr(), t.stride()[0] if B > 1 else 0
 
 
-def _batch_of(t, tail_dims, B, name):
-    if t.dim() > tail_dims and t.shape[0] != B:
-        raise FfdpError(1, "%s has a batch of %d, the tensors %d" % (name, t.shape[0], B))
-
-
-def _rope(fn, x, pos, freq, sections, interleaved, x2, y, y2, stream):
-    _tok(x, "x")
-    if x.dim() != 4:
-        raise FfdpError(1, "x must be (batch, tokens, heads, head_dim)")
-    B, S, _, D = x.shape
-    if not 1 <= len(sections) <= 3:
+def _rope(backward, x, pos, freq, sections, interleaved, x2, y, y2, stream):
+    _tok4(x, "x")
+    B, S, H, D = shape = x.shape
+    axes = len(sections)
+    if not 1 <= axes <= 3:
         raise FfdpError(1, "sections must name one to three axes")
-    pp, psb = _const(pos, "pos", torch.float32, x.device, (S, len(sections)))
-    _batch_of(pos, 2, B, "pos")
-    fp, _ = _const(freq, "freq", torch.float32, x.device, (sum(sections),))
-    if freq.dim() != 1:
-        raise FfdpError(1, "freq must have one axis")
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else _tok(y, "y", x, x.shape)
-    t = (ffdp_rope_tensor * 2)()
-    t[0] = ffdp_rope_tensor(_heads(x), _heads(y), x.shape[2])
+    pp, psb = _const(pos, "pos", torch.float32, x.device, (S, axes), B)
+    fp, _ = _const(freq, "freq", torch.float32, x.device, (sum(sections),), -1)
+    y = x.new_empty(shape) if y is None else _tok4(y, "y", x, shape)
+    s, r = x.stride(), y.stride()
+    t = _ROPE_TENSOR(x.data_ptr(), s[0], s[1], s[2], y.data_ptr(), r[0], r[1], r[2], H)
+    n = 1
     if x2 is not None:
-        _tok(x2, "x2", x)
-        if x2.dim() != 4 or x2.shape[:2] != x.shape[:2] or x2.shape[3] != D:
+        _tok4(x2, "x2", x)
+        shape = x2.shape
+        if shape[0] != B or shape[1] != S or shape[3] != D:
             raise FfdpError(1, "x2 must have x's batch, tokens and head_dim")
-        y2 = torch.empty(x2.shape, dtype=x.dtype, device=x.device) if y2 is None else _tok(y2, "y2", x, x2.shape)
-        t[1] = ffdp_rope_tensor(_heads(x2), _heads(y2), x2.shape[2])
-    p = ffdp_rope_params(B, S, D, len(sections), (ctypes.c_int * 3)(*sections), int(bool(interleaved)))
-    _check(fn(t, 1 if x2 is None else 2, _DTYPES[x.dtype], ctypes.byref(p), pp, psb, fp, _stream(stream)))
+        y2 = x2.new_empty(shape) if y2 is None else _tok4(y2, "y2", x, shape)
+        s, r = x2.stride(), y2.stride()
+        t += _ROPE_TENSOR(x2.data_ptr(), s[0], s[1], s[2], y2.data_ptr(), r[0], r[1], r[2], shape[2])
+        n = 2
+    p = _ROPE_PARAMS(B, S, D, axes, sections[0], sections[1] if axes > 1 else 0, sections[2] if axes > 2 else 0, bool(interleaved))
+    fn = _fast().ffdp_rope_bwd if backward else _fast().ffdp_rope_fwd
+    status = fn(t, n, _DTYPES[x.dtype], p, pp, psb, fp, _stream_of(stream))
+    if status:
+        _check(status)
     return y if x2 is None else (y, y2)
 
 
@@ -533,12 +579,12 @@ def ffdp_rope_fwd(x, pos, freq, sections, interleaved=False, x2=None, y=None, y2
 
     pos: (tokens, axes) or (batch, tokens, axes); freq: (sum(sections),);
     sections: pairs per axis.  Returns y, or (y, y2) with x2; y may be x."""
-    return _rope(lib().ffdp_rope_fwd, x, pos, freq, sections, interleaved, x2, y, y2, stream)
+    return _rope(False, x, pos, freq, sections, interleaved, x2, y, y2, stream)
 
 
 def ffdp_rope_bwd(gy, pos, freq, sections, interleaved=False, gy2=None, gx=None, gx2=None, stream=None):
     """Gradient of ffdp_rope_fwd with respect to its tensors."""
-    return _rope(lib().ffdp_rope_bwd, gy, pos, freq, sections, interleaved, gy2, gx, gx2, stream)
+    return _rope(True, gy, pos, freq, sections, interleaved, gy2, gx, gx2, stream)
 
 
 def attention_params(scale, cap=0.0, causal=False) -> ffdp_attention_params:
@@ -546,49 +592,43 @@ def attention_params(scale, cap=0.0, causal=False) -> ffdp_attention_params:
     return ffdp_attention_params(0, 0, 0, 1, 1, 8, float(scale), float(cap), int(bool(causal)))
 
 
-def _attention_shapes(q, k, v, params):
-    _tok(q, "q")
-    _tok(k, "k", q)
-    _tok(v, "v", q, k.shape)
-    if q.dim() != 4 or k.dim() != 4 or q.shape[0] != k.shape[0] or q.shape[3] != k.shape[3]:
-        raise FfdpError(1, "q and k must be (batch, tokens, heads, head_dim) with one batch and head_dim")
-    return ffdp_attention_params(q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3], params.scale,
-                                 params.cap, params.causal)
+def _attention_shapes(q, k, v, params) -> bytes:
+    _tok4(q, "q")
+    _tok4(k, "k", q)
+    a, b = q.shape, k.shape
+    _tok4(v, "v", q, b)
+    if a[0] != b[0] or a[3] != b[3]:
+        raise FfdpError(1, "q and k must have one batch and head_dim")
+    return _ATTENTION_PARAMS(a[0], a[1], b[1], a[2], b[2], a[3], params.scale, params.cap, params.causal)
 
 
 def _attention_bias(q, k, pos_q, pos_k, slopes, doc_q, doc_k, prefix):
-    if pos_q is None and pos_k is None and slopes is None and doc_q is None and doc_k is None and prefix is None:
+    if slopes is None and pos_q is None and pos_k is None and doc_q is None and doc_k is None and prefix is None:
         return None
-    b, dev, B = ffdp_attention_bias(), q.device, q.shape[0]
+    dev, (B, Sq, Hq, _), Sk = q.device, q.shape, k.shape[1]
+    pq = pk = psb = ksb = sl = dq = dk = dsb = esb = pf = axes = 0
     if slopes is not None:
-        if slopes.dim() != 2 or slopes.shape[0] != q.shape[2] or not 1 <= slopes.shape[1] <= 3:
-            raise FfdpError(1, "slopes must be (q_heads, axes) with one to three axes")
-        b.axes = slopes.shape[1]
-        b.slopes, _ = _const(slopes, "slopes", torch.float32, dev, tuple(slopes.shape))
-    axes = b.axes or 1
+        axes = slopes.shape[-1]
+        sl, _ = _const(slopes, "slopes", torch.float32, dev, (Hq, axes), -1)
     if pos_q is not None:
-        b.pos_q, b.pos_q_sb = _const(pos_q, "pos_q", torch.float32, dev, (q.shape[1], axes))
-        _batch_of(pos_q, 2, B, "pos_q")
+        pq, psb = _const(pos_q, "pos_q", torch.float32, dev, (Sq, axes or 1), B)
     if pos_k is not None:
-        b.pos_k, b.pos_k_sb = _const(pos_k, "pos_k", torch.float32, dev, (k.shape[1], axes))
-        _batch_of(pos_k, 2, B, "pos_k")
+        pk, ksb = _const(pos_k, "pos_k", torch.float32, dev, (Sk, axes or 1), B)
     if doc_q is not None:
-        b.doc_q, b.doc_q_sb = _const(doc_q, "doc_q", torch.int32, dev, (q.shape[1],))
-        _batch_of(doc_q, 1, B, "doc_q")
+        dq, dsb = _const(doc_q, "doc_q", torch.int32, dev, (Sq,), B)
     if doc_k is not None:
-        b.doc_k, b.doc_k_sb = _const(doc_k, "doc_k", torch.int32, dev, (k.shape[1],))
-        _batch_of(doc_k, 1, B, "doc_k")
+        dk, esb = _const(doc_k, "doc_k", torch.int32, dev, (Sk,), B)
     if prefix is not None:
-        b.prefix, _ = _const(prefix, "prefix", torch.int32, dev, (B,))
-    return ctypes.byref(b)
+        pf, _ = _const(prefix, "prefix", torch.int32, dev, (B,), -1)
+    return _ATTENTION_BIAS(pq, pk, psb, ksb, sl, axes, dq, dk, dsb, esb, pf)
 
 
-def _attention_ws(p, backward, ws, device):
+def _attention_ws(p, backward, ws, q):
     if ws is None:
-        n = int(lib().ffdp_attention_workspace_bytes(ctypes.byref(p), backward))
+        n = _fast().ffdp_attention_workspace_bytes(p, backward)
         if n == 0:
             raise FfdpError(1, (lib().ffdp_last_error() or b"").decode())
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws = torch.empty(n, dtype=torch.uint8, device=q.device)
     return ws
 
 
@@ -601,14 +641,19 @@ def ffdp_attention_fwd(q, k, v, params: ffdp_attention_params, pos_q=None, pos_k
     documents (negative: padding); prefix (B,) int32: keys visible to every query of a causal call."""
     p = _attention_shapes(q, k, v, params)
     bias = _attention_bias(q, k, pos_q, pos_k, slopes, doc_q, doc_k, prefix)
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device) if o is None else _tok(o, "o", q, q.shape)
+    shape = q.shape
+    o = q.new_empty(shape) if o is None else _tok4(o, "o", q, shape)
     if lse is None and want_lse:
-        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=q.device)
+        lse = torch.empty((shape[0], shape[2], shape[1]), dtype=torch.float32, device=q.device)
     elif lse is not None:
         _dev(lse, "lse", torch.float32, 3)
-    ws = _attention_ws(p, 0, ws, q.device)
-    _check(lib().ffdp_attention_fwd(_heads(q), _heads(k), _heads(v), _heads(o), _ptr(lse), _DTYPES[q.dtype],
-                                    ctypes.byref(p), bias, _ptr(ws), ws.numel(), _stream(stream)))
+        if tuple(lse.shape) != (shape[0], shape[2], shape[1]):
+            raise FfdpError(1, "lse must be (batch, q_heads, q_len)")
+    ws = _attention_ws(p, 0, ws, q)
+    status = _fast().ffdp_attention_fwd(_heads(q), _heads(k), _heads(v), _heads(o), None if lse is None else lse.data_ptr(),
+                                        _DTYPES[q.dtype], p, bias, ws.data_ptr(), ws.numel(), _stream_of(stream))
+    if status:
+        _check(status)
     return o, lse
 
 
@@ -617,86 +662,106 @@ def ffdp_attention_bwd(q, k, v, o, lse, go, params: ffdp_attention_params, pos_q
     """Gradients (gq, gk, gv) of ffdp_attention_fwd from its o and lse and go = dL/do."""
     p = _attention_shapes(q, k, v, params)
     bias = _attention_bias(q, k, pos_q, pos_k, slopes, doc_q, doc_k, prefix)
-    _tok(o, "o", q, q.shape)
-    _tok(go, "go", q, q.shape)
+    qs, ks = q.shape, k.shape
+    _tok4(o, "o", q, qs)
+    _tok4(go, "go", q, qs)
     _dev(lse, "lse", torch.float32, 3)
-    if tuple(lse.shape) != (q.shape[0], q.shape[2], q.shape[1]):
+    if tuple(lse.shape) != (qs[0], qs[2], qs[1]):
         raise FfdpError(1, "lse must be (batch, q_heads, q_len)")
-    gq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if gq is None else _tok(gq, "gq", q, q.shape)
-    gk = torch.empty(k.shape, dtype=q.dtype, device=q.device) if gk is None else _tok(gk, "gk", q, k.shape)
-    gv = torch.empty(k.shape, dtype=q.dtype, device=q.device) if gv is None else _tok(gv, "gv", q, k.shape)
-    ws = _attention_ws(p, 1, ws, q.device)
-    _check(lib().ffdp_attention_bwd(_heads(q), _heads(k), _heads(v), _heads(o), _ptr(lse), _heads(go), _heads(gq),
-                                    _heads(gk), _heads(gv), _DTYPES[q.dtype], ctypes.byref(p), bias, _ptr(ws),
-                                    ws.numel(), _stream(stream)))
+    gq = q.new_empty(qs) if gq is None else _tok4(gq, "gq", q, qs)
+    gk = k.new_empty(ks) if gk is None else _tok4(gk, "gk", q, ks)
+    gv = v.new_empty(ks) if gv is None else _tok4(gv, "gv", q, ks)
+    ws = _attention_ws(p, 1, ws, q)
+    status = _fast().ffdp_attention_bwd(_heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(), _heads(go), _heads(gq),
+                                        _heads(gk), _heads(gv), _DTYPES[q.dtype], p, bias, ws.data_ptr(), ws.numel(),
+                                        _stream_of(stream))
+    if status:
+        _check(status)
     return gq, gk, gv
 
 
 def _matrix(rows, cols, like):
     """Uninitialised (rows, cols) whose rows start on 16 bytes."""
-    return torch.empty((rows, -(-cols // 8) * 8), dtype=like.dtype, device=like.device)[:, :cols]
+    return like.new_empty((rows, cols)) if cols % 8 == 0 else like.new_empty((rows, cols + 7 & -8))[:, :cols]
 
 
-def _ld(t):
-    return 0 if t is None else t.stride(0)
+def _tok2(t, name, like=None, shape=None):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise FfdpError(1, "%s must have two axes" % name)
+    return _tok(t, name, like, shape)
 
 
 def _linear_shapes(x, w, act):
-    _tok(x, "x")
-    _tok(w, "w", x)
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+    _tok2(x, "x")
+    _tok2(w, "w", x)
+    (M, K), (N, Kw) = x.shape, w.shape
+    if K != Kw:
         raise FfdpError(1, "x must be (rows, in) and w (out, in)")
     if act not in ACTS:
         raise FfdpError(1, "act must be one of %s" % sorted(ACTS))
-    return ffdp_linear_params(x.shape[0], x.shape[1], w.shape[0], ACTS[act])
+    return M, K, N, _LINEAR_PARAMS(M, K, N, ACTS[act])
 
 
-def _linear_ws(p, backward, ws, device):
+def _rows(t):
+    """Pointer and row stride of an optional matrix."""
+    return (None, 0) if t is None else (t.data_ptr(), t.stride()[0])
+
+
+def _linear_ws(p, backward, ws, x):
     if ws is None:
-        n = int(lib().ffdp_linear_workspace_bytes(ctypes.byref(p), backward))
-        ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-    return ws
+        n = _fast().ffdp_linear_workspace_bytes(p, backward)
+        if n == 0:
+            return None, 0, None
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+    return ws.data_ptr(), ws.numel(), ws
 
 
 def ffdp_linear_fwd(x, w, b=None, r=None, act="none", y=None, z=None, ws=None, stream=None, want_z=False):
     """y = act(x w^T + b) + r for x (rows, in), w (out, in): returns (y, z); z, the pre-activation that the
     backward pass of an activation needs, is None unless asked for (or without an activation)."""
-    p = _linear_shapes(x, w, act)
-    M, N = x.shape[0], w.shape[0]
-    if b is not None and _tok(b, "b", x, (N,)).stride(0) != 1 and N > 1:
-        raise FfdpError(1, "b must be contiguous")
+    M, K, N, p = _linear_shapes(x, w, act)
+    shape = (M, N)
+    if b is not None:
+        _tok(b, "b", x, (N,))
     if r is not None:
-        _tok(r, "r", x, (M, N))
-    y = _matrix(M, N, x) if y is None else _tok(y, "y", x, (M, N))
-    if z is None and want_z and act != "none":
+        _tok2(r, "r", x, shape)
+    y = _matrix(M, N, x) if y is None else _tok2(y, "y", x, shape)
+    if z is not None:
+        _tok2(z, "z", x, shape)
+    elif want_z and act != "none":
         z = _matrix(M, N, x)
-    elif z is not None:
-        _tok(z, "z", x, (M, N))
-    ws = _linear_ws(p, 0, ws, x.device)
-    _check(lib().ffdp_linear_fwd(_ptr(x), _ld(x), _ptr(w), _ld(w), _ptr(b), _ptr(r), _ld(r), _ptr(y), _ld(y), _ptr(z),
-                                 _ld(z), _DTYPES[x.dtype], ctypes.byref(p), _ptr(ws), 0 if ws is None else ws.numel(),
-                                 _stream(stream)))
+    wp, wn, ws = _linear_ws(p, 0, ws, x)
+    status = _fast().ffdp_linear_fwd(*_rows(x), *_rows(w), None if b is None else b.data_ptr(), *_rows(r), *_rows(y),
+                                     *_rows(z), _DTYPES[x.dtype], p, wp, wn, _stream_of(stream))
+    if status:
+        _check(status)
     return y, z
 
 
 def ffdp_linear_bwd(x, w, z, gy, act="none", gx=None, gw=None, gb=None, ws=None, stream=None, want_gx=True,
                     want_gw=True, want_gb=True):
     """Gradients (gx, gw, gb) of ffdp_linear_fwd from gy = dL/dy (None where not wanted)."""
-    p = _linear_shapes(x, w, act)
-    M, K, N = x.shape[0], x.shape[1], w.shape[0]
-    _tok(gy, "gy", x, (M, N))
+    M, K, N, p = _linear_shapes(x, w, act)
+    _tok2(gy, "gy", x, (M, N))
     if z is not None:
-        _tok(z, "z", x, (M, N))
-    gx = _matrix(M, K, x) if gx is None and want_gx else gx
-    gw = _matrix(N, K, x) if gw is None and want_gw else gw
-    gb = torch.empty(N, dtype=x.dtype, device=x.device) if gb is None and want_gb else gb
-    for t, n, shape in ((gx, "gx", (M, K)), (gw, "gw", (N, K)), (gb, "gb", (N,))):
-        if t is not None:
-            _tok(t, n, x, shape)
-    ws = _linear_ws(p, 1, ws, x.device)
-    _check(lib().ffdp_linear_bwd(_ptr(x), _ld(x), _ptr(w), _ld(w), _ptr(z), _ld(z), _ptr(gy), _ld(gy), _ptr(gx), _ld(gx),
-                                 _ptr(gw), _ld(gw), _ptr(gb), _DTYPES[x.dtype], ctypes.byref(p), _ptr(ws),
-                                 0 if ws is None else ws.numel(), _stream(stream)))
+        _tok2(z, "z", x, (M, N))
+    if gx is not None:
+        _tok2(gx, "gx", x, (M, K))
+    elif want_gx:
+        gx = _matrix(M, K, x)
+    if gw is not None:
+        _tok2(gw, "gw", x, (N, K))
+    elif want_gw:
+        gw = _matrix(N, K, x)
+    if gb is not None:
+        _tok(gb, "gb", x, (N,))
+    elif want_gb:
+        gb = x.new_empty((N,))
+    wp, wn, ws = _linear_ws(p, 1, ws, x)
+    status = _fast().ffdp_linear_bwd(*_rows(x), *_rows(w), *_rows(z), *_rows(gy), *_rows(gx), *_rows(gw),
+                                     None if gb is None else gb.data_ptr(), _DTYPES[x.dtype], p, wp, wn, _stream_of(stream))
+    if status:
+        _check(status)
     return gx, gw, gb
 
 
