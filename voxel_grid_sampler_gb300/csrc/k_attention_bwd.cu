@@ -12,8 +12,8 @@
 // T2^T (R: resident rows, T: walked rows) go to TMEM, a warpgroup per subtile
 // (one resident row per thread) turns them into P and dS in 16 bits in the
 // same columns, which are the A operands of the accumulating products.  Warps:
-// 0-3 and 4-7 even and odd subtiles, 8 loads (TMA), 9 multiplies, 10 prepares
-// each subtile's lse, delta, positions, documents and non-finite rows.
+// 0-3 and 4-7 even and odd subtiles, 8 loads (TMA), 9 multiplies, 10 and 11
+// prepare each subtile's lse, delta, positions, documents and non-finite rows.
 #include <atomic>
 
 #include "ffdp_attention.cuh"
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       bar_init(tfull + 8 * i, 1);
       bar_init(tempty + 8 * i, 1);
-      bar_init(ready + 8 * i, 1);
+      bar_init(ready + 8 * i, 2);
     }
     for (int s = 0; s < 2; ++s) {
       bar_init(sfull + 8 * s, 1);
@@ -215,56 +215,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(accfull);
     mma_commit(drain);
     bar_drain(drain, 0);
-  } else if (warp == 10) {
+  } else if (warp >= 10) {
     Ring<kStages> r;
+    const int e = (warp - 10) * 32 + lane;  // token of the subtile
+    const bool hide = a.causal || a.doc_q;  // past the last token a subtile holds zeros anyway
     for (; cur.head < heads; cur = next(cur)) {
-      const int h = h0 + cur.head;
-      const bool masked = cur.code == kMasked;
-      float lse[2], delta[2], pos[2][3];
-      int doc[2], limit[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int y = cur.n * kSub + i * 32 + lane;
-        const bool in = y < walk;
-        if (KV) {
-          const int64_t at = ((int64_t)b * a.Hq + h) * a.Sq + y;
-          const float v = in ? a.lse[at] : INFINITY;
-          lse[i] = v == -INFINITY ? INFINITY : v * kLog2e;  // no key seen: P = 2^(score - inf) = 0
-          delta[i] = in && v != -INFINITY ? a.delta[at] : 0.0f;
-          limit[i] = masked ? key_limit(a, prefix, y) : 0;
-        }
-        if (AXES) {
-          const float* pp = KV ? a.pos_q + b * a.pos_q_sb : a.pos_k + b * a.pos_k_sb;
-#pragma unroll
-          for (int x = 0; x < 3; ++x)
-            pos[i][x] = x < a.axes && in ? pp[(int64_t)y * a.axes + x] * (a.slopes[h * a.axes + x] * kLog2e) : 0.0f;
-        }
-        doc[i] = a.doc_q && masked && in ? max(KV ? a.doc_q[b * a.doc_q_sb + y] : a.doc_k[b * a.doc_k_sb + y], -1) : -1;
+      const int h = h0 + cur.head, y = cur.n * kSub + e;
+      const bool masked = cur.code == kMasked, in = y < walk;
+      float lse = 0.0f, delta = 0.0f, pos[3];
+      int limit = 0;
+      if (KV) {
+        const int64_t at = ((int64_t)b * a.Hq + h) * a.Sq + y;
+        const float v = in ? a.lse[at] : INFINITY;
+        lse = v == -INFINITY ? INFINITY : v * kLog2e;  // no key seen: P = 2^(score - inf) = 0
+        delta = in && v != -INFINITY ? a.delta[at] : 0.0f;
+        limit = masked ? key_limit(a, prefix, y) : 0;
       }
+      if (AXES) {
+        const float* pp = KV ? a.pos_q + b * a.pos_q_sb : a.pos_k + b * a.pos_k_sb;
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+          pos[x] = x < a.axes && in ? pp[(int64_t)y * a.axes + x] * (a.slopes[h * a.axes + x] * kLog2e) : 0.0f;
+      }
+      const int doc = a.doc_q && masked && in ? max(KV ? a.doc_q[b * a.doc_q_sb + y] : a.doc_k[b * a.doc_k_sb + y], -1) : -1;
       if (!bar_wait_warp(tfull + 8 * r.slot, r.phase, guard)) break;
       Aux& x = aux[r.slot];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int e = i * 32 + lane;
-        if (KV) {
-          x.lse[e] = lse[i];
-          x.delta[e] = delta[i];
-          x.limit[e] = limit[i];
-        }
-        if (AXES) {
-#pragma unroll
-          for (int c = 0; c < 3; ++c) x.pos[c][e] = pos[i][c];
-        }
-        x.doc[e] = doc[i];
-        if (masked) {
-          char* t = st + r.slot * 2 * sub_bytes;
-          bool bad = clear_bad_row<T>(t, f.panels, kSubPanel, e);
-          if (KV) bad |= clear_bad_row<T>(t + sub_bytes, f.panels, kSubPanel, e);
-          const unsigned m = __ballot_sync(0xffffffffu, bad);
-          if (lane == 0) x.bad[i] = m;
-        }
+      if (KV) {
+        x.lse[e] = lse;
+        x.delta[e] = delta;
+        x.limit[e] = limit;
       }
-      if (masked) fence_async_smem();
+      if (AXES) {
+#pragma unroll
+        for (int c = 0; c < 3; ++c) x.pos[c][e] = pos[c];
+      }
+      x.doc[e] = doc;
+      if (masked) {
+        bool bad = false;
+        if (hide) {
+          char* t = st + r.slot * 2 * sub_bytes;
+          bad = clear_bad_row<T>(t, f.panels, kSubPanel, e);
+          if (KV) bad |= clear_bad_row<T>(t + sub_bytes, f.panels, kSubPanel, e);
+          fence_async_smem();
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, bad);
+        if (lane == 0) x.bad[warp - 10] = m;
+      }
       __syncwarp();
       if (lane == 0) bar_arrive(ready + 8 * r.slot);
       r.next();

@@ -381,24 +381,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = bar_wait_warp(vfull + 8 * slot, phase, guard))) break;
           Aux& x = aux[slot];
           if (AXES && PACKED) {
-  #pragma unroll
+#pragma unroll
             for (int i = 0; i < 4; ++i)
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < 3; ++c) x.pos[0][c][i * 32 + lane] = pos[i][c];
           } else if (AXES) {
             float lo[3], hi[3];
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < 3; ++c) {
               lo[c] = warp_min(fminf(fminf(pos[0][c], pos[1][c]), fminf(pos[2][c], pos[3][c])));
               hi[c] = warp_max(fmaxf(fmaxf(pos[0][c], pos[1][c]), fmaxf(pos[2][c], pos[3][c])));
             }
-  #pragma unroll
+#pragma unroll
             for (int t = 0; t < 2; ++t) {
               float fold[4] = {};
-  #pragma unroll
+#pragma unroll
               for (int c = 0; c < 3; ++c) {
                 const float side = lo[c] >= qhi[t][c] ? 1.0f : (hi[c] <= qlo[t][c] ? -1.0f : 0.0f);
-  #pragma unroll
+#pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const float k = (pos[i][c] - origin[t][c]) * slope[t][c];
                   fold[i] = fmaf(-side, k, fold[i]);
@@ -406,12 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) x.side[t][c] = side;
               }
-  #pragma unroll
+#pragma unroll
               for (int i = 0; i < 4; ++i) x.fold[t][i * 32 + lane] = fold[i];
             }
           }
-          if (masked) {
-  #pragma unroll
+          if (masked && (a.causal || a.doc_k)) {  // past the last key the tile holds zeros anyway
+#pragma unroll
             for (int i = 0; i < 4; ++i) {
               x.doc[i * 32 + lane] = doc[i];
               const unsigned m =
@@ -458,11 +458,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return valid;
       };
       float sl[PACKED ? 4 : 1][3];  // rows of several heads: each row's slopes
+      bool busy;
       {
         const int r = (warp % 4) * 32 + lane;
         int i, h;
-        place(r, &i, &h);
-        __syncwarp();
+        busy = __any_sync(0xffffffffu, place(r, &i, &h));
         rowlimit[t][r] = key_limit(a, prefix_of(a, b), i);
         const int d = a.doc_q ? a.doc_q[b * a.doc_q_sb + i] : 0;
         rowdoc[t][r] = d < 0 ? -2 : d;  // padded keys are -1: equal to no query
@@ -503,6 +503,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Aux& x = aux[slot];
           if (!(ok = bar_wait_warp(sfull + 8 * t, count & 1u, guard))) break;
           fence_after();
+          if (!busy) {  // no row of this warp exists: its lanes of P are never read out
+            if (own_p && lane == 0) bar_arrive(sread + 8 * t);
+            // not before the others' arrivals for the last tile were consumed
+            if (own_p && count && !(ok = bar_wait_warp(pvdone + 8 * t, (count - 1) & 1u, guard))) break;
+            if (lane == 0) bar_arrive(pfull + 8 * t);
+            ++count;
+            first = false;
+            if (++slot == NS) slot = 0, phase ^= 1u;
+            continue;
+          }
           f32x2 v[4][16];  // rows by pairs of keys
           {
             float s[128];
@@ -537,24 +547,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           float shift[4] = {};  // of whole rows
           const float sc = CAP ? 1.0f : f.c;
           if (AXES && PACKED) {
+            const f32x2 sc2 = pair(sc, sc);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int g = 0; g < 16; ++g) v[y][g] = mul2(v[y][g], sc2);
 #pragma unroll 1
-            for (int ax = 0; ax < 3; ++ax) {
+            for (int ax = 0; ax < a.axes; ++ax) {
               const float* kp = x.pos[0][ax] + cb;
-              float p[4], q[4];
+              f32x2 np[4], q[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                p[y] = rowpos[t][ax][r0 + 8 * y];
-                q[y] = ax == 0 ? sl[PACKED ? y : 0][0] : (ax == 1 ? sl[PACKED ? y : 0][1] : sl[PACKED ? y : 0][2]);
+                const float p = -rowpos[t][ax][r0 + 8 * y];
+                const float z = ax == 0 ? sl[PACKED ? y : 0][0] : (ax == 1 ? sl[PACKED ? y : 0][1] : sl[PACKED ? y : 0][2]);
+                np[y] = pair(p, p);
+                q[y] = pair(z, z);
               }
 #pragma unroll
               for (int g = 0; g < 16; ++g) {
-                const float2 kk = *reinterpret_cast<const float2*>(kp + 8 * g);
+                const f32x2 kk = *reinterpret_cast<const f32x2*>(kp + 8 * g);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  float2 z = split(v[y][g]);
-                  if (ax == 0) z.x *= sc, z.y *= sc;
-                  v[y][g] = pair(fmaf(-q[y], fabsf(p[y] - kk.x), z.x), fmaf(-q[y], fabsf(p[y] - kk.y), z.y));
-                }
+                for (int y = 0; y < 4; ++y) v[y][g] = fma2(neg_abs2(add2(kk, np[y])), q[y], v[y][g]);
               }
             }
           } else if (AXES) {
@@ -616,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
             }
-            if (x.bad[0] | x.bad[1] | x.bad[2] | x.bad[3]) {  // a visible non-finite value makes the row NaN
+            if ((a.causal || a.doc_q) && (x.bad[0] | x.bad[1] | x.bad[2] | x.bad[3])) {  // a visible non-finite value makes the row NaN
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
                 bool poison = false;
