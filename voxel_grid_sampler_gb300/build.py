@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libffdp.so")
 SOURCES = ["ffdp_api.cu", "k_sweep.cu", "k_lncc.cu", "k_lncc_wide.cu", "k_channels.cu", "k_reg.cu",
-           "ffdp_tokens_api.cu", "k_rope.cu", "k_attention_fwd.cu", "k_attention_bwd.cu", "k_linear.cu"]
+           "ffdp_tokens_api.cu", "k_rope.cu", "k_attention_fwd.cu", "k_attention_few.cu",
+           "k_attention_bwd.cu", "k_linear.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

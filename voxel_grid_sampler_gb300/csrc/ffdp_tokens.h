@@ -68,11 +68,19 @@ struct AttnArgs {
 };
 // Query tiles of the forward pass, their packing and splits, workspace parts.
 struct AttnPlan {
+  int few;             // at most 16 rows per key head: k_attention_few.cu
   int packed, rh, gb, tiles, pairs, splits, nq, nk;
   size_t ranges_bytes, part_bytes;
 };
 AttnPlan attention_plan(const AttnArgs& a, int sms);
 cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, int sms, void* ws, cudaStream_t s);
+struct FewArgs {
+  int splits;
+  float c, cap_in, cap2;  // scale log2 e; 2 log2 e scale / cap, cap log2 e
+  float* part;            // as the forward kernel's
+};
+int few_splits(int64_t pairs, int64_t keys, int sms);
+cudaError_t launch_attention_few(int dt, const AttnArgs& a, const FewArgs& f, cudaStream_t s);
 size_t attention_bwd_bytes(const AttnArgs& a);
 cudaError_t launch_attention_bwd(int dt, const AttnArgs& a, void* ws, cudaStream_t s);
 

@@ -793,14 +793,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the splits of a row: o = sum 2^(lse_s - lse) o_s.  One warp per row.
 template <class T>
-__global__ void __launch_bounds__(256) k_attn_join(const FwdArgs f) {
-  const AttnArgs& a = f.a;
+__global__ void __launch_bounds__(256) k_attn_join(const AttnArgs a, int splits, const float* part) {
   const int64_t rows = (int64_t)a.B * a.Hq * a.Sq, row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
   if (row >= rows) return;
   const int lane = threadIdx.x % 32;
-  const float* ls = f.part + rows * a.D * f.splits;
+  const float* ls = part + rows * a.D * splits;
   float top = -INFINITY;
-  for (int s = lane; s < f.splits; s += 32) {
+  for (int s = lane; s < splits; s += 32) {
     const float v = ls[s * rows + row];
     top = v > top || v != v ? v : top;
   }
@@ -811,11 +810,11 @@ __global__ void __launch_bounds__(256) k_attn_join(const FwdArgs f) {
   }
   const float ref = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f, acc[4] = {};
-  for (int s = 0; s < f.splits; ++s) {
+  for (int s = 0; s < splits; ++s) {
     const float w = ex2(ls[s * rows + row] - ref);
     sum += w;
     if (4 * lane < a.D) {
-      const float4 o = *reinterpret_cast<const float4*>(f.part + (s * rows + row) * a.D + 4 * lane);
+      const float4 o = *reinterpret_cast<const float4*>(part + (s * rows + row) * a.D + 4 * lane);
       acc[0] = fmaf(w, o.x, acc[0]);
       acc[1] = fmaf(w, o.y, acc[1]);
       acc[2] = fmaf(w, o.z, acc[2]);
@@ -873,12 +872,15 @@ cudaError_t run(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap&
   note_launch_begin("k_attn_fwd", s);
   k_attn_fwd<T, AXES, CAP, PACKED><<<grid, kThreads, smem, s>>>(mq, mk, mv, f);
   note_launch_end(s);
-  if (f.splits > 1) {
-    const int64_t rows = (int64_t)f.a.B * f.a.Hq * f.a.Sq;
-    note_launch_begin("k_attn_join", s);
-    k_attn_join<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(f);
-    note_launch_end(s);
-  }
+  return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t join(const AttnArgs& a, int splits, const float* part, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
+  note_launch_begin("k_attn_join", s);
+  k_attn_join<T><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a, splits, part);
+  note_launch_end(s);
   return cudaGetLastError();
 }
 
@@ -912,6 +914,7 @@ AttnPlan attention_plan(const AttnArgs& a, int sms) {
   AttnPlan p{};
   p.nq = (a.Sq + kTile - 1) / kTile;
   p.nk = (a.Sk + kTile - 1) / kTile;
+  p.few = a.Sq > 0 && (int64_t)a.G * a.Sq <= 16;
   p.packed = a.Sq > 0 && a.Sq <= kTile / 2 && a.G > 1;
   if (p.packed) {
     p.rh = a.Sq;
@@ -929,6 +932,7 @@ AttnPlan attention_plan(const AttnArgs& a, int sms) {
   const int64_t least = (p.nk + kMaxCodes - 1) / kMaxCodes;
   if (s < least) s = least;
   p.splits = (int)(s < 1 ? 1 : s);
+  if (p.few) p.splits = few_splits((int64_t)a.B * a.Hk, a.Sk, sms);
   const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
   p.ranges_bytes = round256((size_t)a.B * p.nq * sizeof(DocRange)) + round256((size_t)a.B * p.nk * sizeof(DocRange));
   p.part_bytes = p.splits > 1 ? round256((size_t)rows * p.splits * (a.D + 1) * 4) : 0;
@@ -943,7 +947,20 @@ cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, int sms, void* ws, c
   DocRange* dq = reinterpret_cast<DocRange*>(w);
   DocRange* dk = reinterpret_cast<DocRange*>(w + round256((size_t)a.B * p.nq * sizeof(DocRange)));
   f.part = reinterpret_cast<float*>(w + p.ranges_bytes);
-  if (a.doc_q) {
+  if (p.few) {
+    FewArgs x{};
+    x.splits = p.splits;
+    x.c = a.scale * kLog2e;
+    if (a.cap > 0.0f) {
+      x.cap_in = 2.0f * kLog2e * a.scale / a.cap;
+      x.cap2 = a.cap * kLog2e;
+    }
+    x.part = f.part;
+    const cudaError_t e = launch_attention_few(dt, a, x, s);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    FFDP_TOK_SWITCH16(dt, T, { return join<T>(a, p.splits, f.part, s); });
+  }
+  if (a.doc_q && !p.few) {
     f.dq = dq;
     f.dk = dk;
     const cudaError_t e = launch_doc_ranges(a, dq, dk, s);
@@ -982,7 +999,9 @@ cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, int sms, void* ws, c
   if (e == cudaSuccess) e = heads_map(&mk, dt, k, a.B, a.Sk, a.Hk, a.D, kTile, 1);
   if (e == cudaSuccess) e = heads_map(&mv, dt, v, a.B, a.Sk, a.Hk, a.D, kTile, 1);
   if (e != cudaSuccess) return e;
-  FFDP_TOK_SWITCH16(dt, T, { return pick<T>(mq, mk, mv, f, s); });
+  FFDP_TOK_SWITCH16(dt, T, { e = pick<T>(mq, mk, mv, f, s); });
+  if (e != cudaSuccess || p.splits == 1) return e;
+  FFDP_TOK_SWITCH16(dt, T, { return join<T>(a, p.splits, f.part, s); });
 }
 
 }  // namespace ffdp

@@ -14,11 +14,40 @@ namespace {
 
 using namespace tc;
 
+// erfc(x) e^(x^2) for x >= 0 by Abramowitz and Stegun 7.1.26 (|error| of erf
+// below 1.5e-7): a polynomial in t = 1 / (1 + 0.3275911 x).
+__device__ __forceinline__ float erfc_poly(float t) {
+  float y = fmaf(t, 1.061405429f, -1.453152027f);
+  y = fmaf(t, y, 1.421413741f);
+  y = fmaf(t, y, -0.284496736f);
+  y = fmaf(t, y, 0.254829592f);
+  return t * y;
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcpf(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Phi(z), the normal distribution's integral: half of erfc(|z| / sqrt 2) on
+// the negative side, without cancellation, and one minus that on the other.
+__device__ __forceinline__ float normal_cdf(float z) {
+  const float t = rcpf(fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.0f));
+  const float h = 0.5f * erfc_poly(t) * ex2f(z * z * -0.72134752f);
+  return z < 0.0f ? h : 1.0f - h;
+}
+
 __device__ __forceinline__ float act_fwd(int act, float z) {
   switch (act) {
     case 1: return z > 0.0f ? z : (z == z ? 0.0f : z);
-    case 2: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case 3: return __fdividef(z, 1.0f + __expf(-z));
+    case 2: return z * normal_cdf(z);
+    case 3: return z * rcpf(1.0f + ex2f(z * -1.44269504f));
     default: return z;
   }
 }
@@ -26,10 +55,10 @@ __device__ __forceinline__ float act_fwd(int act, float z) {
 __device__ __forceinline__ float act_grad(int act, float z) {
   switch (act) {
     case 1: return z > 0.0f ? 1.0f : 0.0f;
-    case 2: return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * expf(-0.5f * z * z) * 0.39894228f;
+    case 2: return fmaf(z * 0.39894228f, ex2f(z * z * -0.72134752f), normal_cdf(z));
     case 3: {
-      const float g = 1.0f / (1.0f + expf(-z));
-      return g * (1.0f + z * (1.0f - g));
+      const float g = rcpf(1.0f + ex2f(z * -1.44269504f));
+      return g * fmaf(z, 1.0f - g, 1.0f);
     }
     default: return 1.0f;
   }
@@ -268,25 +297,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<NST> r;
     Ring<2> acc;
     bool ok = true;
-    const uint32_t step_a = p.a_mn ? 2048 : 32, step_b = p.b_mn ? 2048 : 32;
+    // low words of the first slot's descriptors, in units of 16 bytes
+    const uint32_t a0 = (uint32_t)smem_desc(sm, 8192, 1024), b0 = (uint32_t)smem_desc(sm + kBM * kBK * 2, 8192, 1024);
+    const uint32_t hi = (uint32_t)(smem_desc(0, 8192, 1024) >> 32);
+    const uint32_t step_a = p.a_mn ? 128 : 2, step_b = p.b_mn ? 128 : 2;
     for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
       int tm, tn, k0, k1;
       work_item(p, w, &tm, &tn, &k0, &k1);
       if (!bar_wait(acce + 8 * acc.slot, acc.phase ^ 1u, g)) break;
       fence_after();
       const uint32_t d = tmem + acc.slot * BN;
+      bool add = false;
       for (int k = k0; k < k1; ++k) {
         if (!bar_wait(full + 8 * r.slot, r.phase, g)) {
           ok = false;
           break;
         }
         fence_after();
-        const uint32_t a = sm + r.slot * SB, b = a + kBM * kBK * 2;
-        const uint64_t da = smem_desc(a, 8192, 1024), db = smem_desc(b, 8192, 1024);
-#pragma unroll
-        for (int i = 0; i < kBK / 16; ++i)
-          mma_ss(d, da + ((i * step_a) >> 4), db + ((i * step_b) >> 4), p.idesc, k > k0 || i > 0);
+        const uint32_t a = a0 + r.slot * (SB >> 4), b = b0 + r.slot * (SB >> 4);
+        mma_ss(d, a, hi, b, hi, p.idesc, add);
+        mma_ss(d, a + step_a, hi, b + step_b, hi, p.idesc, true);
+        mma_ss(d, a + 2 * step_a, hi, b + 2 * step_b, hi, p.idesc, true);
+        mma_ss(d, a + 3 * step_a, hi, b + 3 * step_b, hi, p.idesc, true);
         mma_commit(empty + 8 * r.slot);
+        add = true;
         r.next();
       }
       mma_commit(accf + 8 * acc.slot);
