@@ -393,31 +393,88 @@ __global__ void __launch_bounds__(256) k_product_join(const Product p) {
   finish<T, CW>(p, v, m0, n0, patches + warp * 32 * CW * 2, lane);
 }
 
-// One thread per column and chunk of rows.
-template <class T>
-__global__ void __launch_bounds__(128) k_linear_gz(const LinearGradArgs a, int rows) {
-  const int n = blockIdx.x * 128 + threadIdx.x;
-  if (n >= a.N) return;
-  const int m0 = blockIdx.y * rows, m1 = min(a.M, m0 + rows);
-  float sum = 0.0f;
-  for (int64_t m = m0; m < m1; ++m) {
-    float g = to_f32<T>(static_cast<const T*>(a.gy)[m * a.ldgy + n]);
-    if (a.gz) {
-      g *= act_grad(a.act, to_f32<T>(static_cast<const T*>(a.z)[m * a.ldz + n]));
-      static_cast<T*>(a.gz)[m * a.ldgz + n] = from_f32<T>(g);
-    }
-    sum += g;
-  }
-  if (a.partial) a.partial[(int64_t)blockIdx.y * a.N + n] = sum;
-}
+// gz and partial column sums of a chunk of rows: a thread has 8 columns, a
+// warp 256; the CTA's 8 warps take rows in turn and add their sums in order.
+constexpr int kGzCols = 256, kGzWarps = 8;
 
 template <class T>
-__global__ void __launch_bounds__(128) k_linear_gb(const LinearGradArgs a) {
-  const int n = blockIdx.x * 128 + threadIdx.x;
-  if (n >= a.N) return;
-  float sum = 0.0f;
-  for (int c = 0; c < a.chunks; ++c) sum += a.partial[(int64_t)c * a.N + n];
-  static_cast<T*>(a.gb)[n] = from_f32<T>(sum);
+__global__ void __launch_bounds__(kGzWarps * 32) k_linear_gz(const LinearGradArgs a, int rows) {
+  __shared__ float sums[kGzWarps][kGzCols];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, n = blockIdx.x * kGzCols + lane * 8;
+  const int m0 = blockIdx.y * rows, m1 = min(a.M, m0 + rows);
+  const T *gy = static_cast<const T*>(a.gy), *z = static_cast<const T*>(a.z);
+  T* gz = static_cast<T*>(a.gz);
+  float sum[8] = {};
+  if (n + 8 <= a.N) {
+#pragma unroll 4
+    for (int m = m0 + warp; m < m1; m += kGzWarps) {
+      const uint4 u = *reinterpret_cast<const uint4*>(gy + (int64_t)m * a.ldgy + n);
+      const uint32_t gw[4] = {u.x, u.y, u.z, u.w};
+      float g[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = Pair<T>::unpack(gw[k]);
+        g[2 * k] = f.x;
+        g[2 * k + 1] = f.y;
+      }
+      if (gz) {
+        const uint4 v = *reinterpret_cast<const uint4*>(z + (int64_t)m * a.ldz + n);
+        const uint32_t zw[4] = {v.x, v.y, v.z, v.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = Pair<T>::unpack(zw[k]);
+          g[2 * k] *= act_grad(a.act, f.x);
+          g[2 * k + 1] *= act_grad(a.act, f.y);
+          o[k] = Pair<T>::pack(g[2 * k], g[2 * k + 1]);
+        }
+        *reinterpret_cast<uint4*>(gz + (int64_t)m * a.ldgz + n) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += g[k];
+    }
+  } else if (n < a.N) {
+    for (int m = m0 + warp; m < m1; m += kGzWarps)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (n + k >= a.N) continue;
+        float g = to_f32<T>(gy[(int64_t)m * a.ldgy + n + k]);
+        if (gz) {
+          g *= act_grad(a.act, to_f32<T>(z[(int64_t)m * a.ldz + n + k]));
+          gz[(int64_t)m * a.ldgz + n + k] = from_f32<T>(g);
+        }
+        sum[k] += g;
+      }
+  }
+  if (!a.partial) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sums[warp][lane * 8 + k] = sum[k];
+  __syncthreads();
+  const int c = threadIdx.x, col = blockIdx.x * kGzCols + c;
+  if (col >= a.N) return;
+  float t = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kGzWarps; ++w) t += sums[w][c];
+  a.partial[(int64_t)blockIdx.y * a.N + col] = t;
+}
+
+// Sums of the chunks, 32 columns per CTA, 8 threads per column.
+template <class T>
+__global__ void __launch_bounds__(256) k_linear_gb(const LinearGradArgs a) {
+  __shared__ float sums[8][32];
+  const int c = threadIdx.x % 32, w = threadIdx.x / 32, n = blockIdx.x * 32 + c;
+  float t = 0.0f;
+  if (n < a.N) {
+#pragma unroll 8
+    for (int i = w; i < a.chunks; i += 8) t += a.partial[(int64_t)i * a.N + n];
+  }
+  sums[w][c] = t;
+  __syncthreads();
+  if (w || n >= a.N) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v += sums[i][c];
+  static_cast<T*>(a.gb)[n] = from_f32<T>(v);
 }
 
 template <class T, int BN>
@@ -507,22 +564,23 @@ cudaError_t launch_linear(int dt, const LinearArgs& a, int sms, float* partial, 
   });
 }
 
+// Chunks of rows: four CTAs per SM, at least 16 rows each (two per warp).
 int linear_grad_chunks(int M, int N, int sms) {
-  const int cols = (N + 127) / 128;
-  int c = (sms * 8 + cols - 1) / cols;
-  const int most = (M + 31) / 32;
+  const int cols = div_up(N, kGzCols);
+  int c = div_up(4 * (int64_t)sms, cols);
+  const int most = div_up(M, 2 * kGzWarps);
   c = c < most ? c : most;
   return c < 1 ? 1 : c;
 }
 
 cudaError_t launch_linear_grad(int dt, const LinearGradArgs& a, cudaStream_t s) {
-  const int cols = (a.N + 127) / 128, rows = (a.M + a.chunks - 1) / a.chunks;
+  const int rows = div_up(a.M, a.chunks);
   note_launch_begin("k_linear_gz", s);
-  FFDP_TOK_SWITCH16(dt, T, (k_linear_gz<T><<<dim3(cols, a.chunks), 128, 0, s>>>(a, rows)));
+  FFDP_TOK_SWITCH16(dt, T, (k_linear_gz<T><<<dim3(div_up(a.N, kGzCols), a.chunks), kGzWarps * 32, 0, s>>>(a, rows)));
   note_launch_end(s);
   if (a.gb) {
     note_launch_begin("k_linear_gb", s);
-    FFDP_TOK_SWITCH16(dt, T, (k_linear_gb<T><<<cols, 128, 0, s>>>(a)));
+    FFDP_TOK_SWITCH16(dt, T, (k_linear_gb<T><<<div_up(a.N, 32), 256, 0, s>>>(a)));
     note_launch_end(s);
   }
   return cudaGetLastError();
