@@ -507,9 +507,10 @@ def _stream_of(stream) -> int:
 def _tok(t, name, like=None, shape=None):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise FfdpError(1, "%s must be a CUDA tensor" % name)
-    if t.dtype not in _DTYPES:
-        raise FfdpError(1, "%s must be float32, float16 or bfloat16, got %s" % (name, t.dtype))
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if like is None:
+        if t.dtype not in _DTYPES:
+            raise FfdpError(1, "%s must be float32, float16 or bfloat16, got %s" % (name, t.dtype))
+    elif t.dtype != like.dtype or t.get_device() != like.get_device():
         raise FfdpError(1, "%s must have the type and device of the first tensor" % name)
     if shape is not None and t.shape != shape:
         raise FfdpError(1, "%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
@@ -553,7 +554,7 @@ def _rope(backward, x, pos, freq, sections, interleaved, x2, y, y2, stream):
         raise FfdpError(1, "sections must name one to three axes")
     pp, psb = _const(pos, "pos", torch.float32, x.device, (S, axes), B)
     fp, _ = _const(freq, "freq", torch.float32, x.device, (sum(sections),), -1)
-    y = x.new_empty(shape) if y is None else _tok4(y, "y", x, shape)
+    y = torch.empty(shape, dtype=x.dtype, device=x.device) if y is None else _tok4(y, "y", x, shape)
     s, r = x.stride(), y.stride()
     t = _ROPE_TENSOR(x.data_ptr(), s[0], s[1], s[2], y.data_ptr(), r[0], r[1], r[2], H)
     n = 1
@@ -562,7 +563,7 @@ def _rope(backward, x, pos, freq, sections, interleaved, x2, y, y2, stream):
         shape = x2.shape
         if shape[0] != B or shape[1] != S or shape[3] != D:
             raise FfdpError(1, "x2 must have x's batch, tokens and head_dim")
-        y2 = x2.new_empty(shape) if y2 is None else _tok4(y2, "y2", x, shape)
+        y2 = torch.empty(shape, dtype=x2.dtype, device=x2.device) if y2 is None else _tok4(y2, "y2", x, shape)
         s, r = x2.stride(), y2.stride()
         t += _ROPE_TENSOR(x2.data_ptr(), s[0], s[1], s[2], y2.data_ptr(), r[0], r[1], r[2], shape[2])
         n = 2
@@ -642,7 +643,7 @@ def ffdp_attention_fwd(q, k, v, params: ffdp_attention_params, pos_q=None, pos_k
     p = _attention_shapes(q, k, v, params)
     bias = _attention_bias(q, k, pos_q, pos_k, slopes, doc_q, doc_k, prefix)
     shape = q.shape
-    o = q.new_empty(shape) if o is None else _tok4(o, "o", q, shape)
+    o = torch.empty(shape, dtype=q.dtype, device=q.device) if o is None else _tok4(o, "o", q, shape)
     if lse is None and want_lse:
         lse = torch.empty((shape[0], shape[2], shape[1]), dtype=torch.float32, device=q.device)
     elif lse is not None:
@@ -668,9 +669,9 @@ def ffdp_attention_bwd(q, k, v, o, lse, go, params: ffdp_attention_params, pos_q
     _dev(lse, "lse", torch.float32, 3)
     if tuple(lse.shape) != (qs[0], qs[2], qs[1]):
         raise FfdpError(1, "lse must be (batch, q_heads, q_len)")
-    gq = q.new_empty(qs) if gq is None else _tok4(gq, "gq", q, qs)
-    gk = k.new_empty(ks) if gk is None else _tok4(gk, "gk", q, ks)
-    gv = v.new_empty(ks) if gv is None else _tok4(gv, "gv", q, ks)
+    gq = torch.empty(qs, dtype=q.dtype, device=q.device) if gq is None else _tok4(gq, "gq", q, qs)
+    gk = torch.empty(ks, dtype=k.dtype, device=k.device) if gk is None else _tok4(gk, "gk", q, ks)
+    gv = torch.empty(ks, dtype=v.dtype, device=v.device) if gv is None else _tok4(gv, "gv", q, ks)
     ws = _attention_ws(p, 1, ws, q)
     status = _fast().ffdp_attention_bwd(_heads(q), _heads(k), _heads(v), _heads(o), lse.data_ptr(), _heads(go), _heads(gq),
                                         _heads(gk), _heads(gv), _DTYPES[q.dtype], p, bias, ws.data_ptr(), ws.numel(),
@@ -682,7 +683,7 @@ def ffdp_attention_bwd(q, k, v, o, lse, go, params: ffdp_attention_params, pos_q
 
 def _matrix(rows, cols, like):
     """Uninitialised (rows, cols) whose rows start on 16 bytes."""
-    return like.new_empty((rows, cols)) if cols % 8 == 0 else like.new_empty((rows, cols + 7 & -8))[:, :cols]
+    return torch.empty_strided((rows, cols), (cols + 7 & -8, 1), dtype=like.dtype, device=like.device)
 
 
 def _tok2(t, name, like=None, shape=None):
@@ -756,7 +757,7 @@ def ffdp_linear_bwd(x, w, z, gy, act="none", gx=None, gw=None, gb=None, ws=None,
     if gb is not None:
         _tok(gb, "gb", x, (N,))
     elif want_gb:
-        gb = x.new_empty((N,))
+        gb = torch.empty((N,), dtype=x.dtype, device=x.device)
     wp, wn, ws = _linear_ws(p, 1, ws, x)
     status = _fast().ffdp_linear_bwd(*_rows(x), *_rows(w), *_rows(z), *_rows(gy), *_rows(gx), *_rows(gw),
                                      None if gb is None else gb.data_ptr(), _DTYPES[x.dtype], p, wp, wn, _stream_of(stream))
