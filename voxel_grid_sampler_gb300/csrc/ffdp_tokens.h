@@ -101,7 +101,7 @@ struct LinearArgs {
   int act;
 };
 struct LinearPlan {
-  int bn, splits;
+  int pair, bn, splits;
   size_t partial_bytes;
 };
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int sms);

@@ -86,11 +86,15 @@ constexpr int kBM = 128, kBK = 64;
 constexpr int kThreads = 384;  // warp 0 loads, warp 1 multiplies, warps 4-11 run the epilogue
 constexpr int kEpiWarps = 8;
 
-__host__ __device__ constexpr int stages(int BN) { return BN == 256 ? 4 : 6; }
-__host__ __device__ constexpr int stage_bytes(int BN) { return (kBM + BN) * kBK * 2; }
+// Of a pair of CTAs each loads its half of B's rows (BN / 2).
+__host__ __device__ constexpr int b_rows(int BN, bool PAIR) { return PAIR ? BN / 2 : BN; }
+__host__ __device__ constexpr int stages(int BN, bool PAIR) { return BN == 256 && !PAIR ? 4 : 6; }
+__host__ __device__ constexpr int stage_bytes(int BN, bool PAIR) { return (kBM + b_rows(BN, PAIR)) * kBK * 2; }
 __host__ __device__ constexpr int chunk_cols(int BN) { return BN / 2 < 64 ? BN / 2 : 64; }
 __host__ __device__ constexpr int stage_out_bytes(int BN) { return kEpiWarps * 32 * chunk_cols(BN) * 2; }
-constexpr size_t smem_bytes(int BN) { return 1024 + (size_t)stages(BN) * stage_bytes(BN) + stage_out_bytes(BN) + 256; }
+constexpr size_t smem_bytes(int BN, bool PAIR) {
+  return 1024 + (size_t)stages(BN, PAIR) * stage_bytes(BN, PAIR) + stage_out_bytes(BN) + 256;
+}
 
 struct Product {
   int M, N, K;
@@ -227,10 +231,15 @@ __device__ __forceinline__ void finish(const Product& p, float* v, int m0, int n
   flush(p.c, p.ldc);
 }
 
-template <class T, int BN>
+// One CTA per SM, or pairs of CTAs (clusters of two) that share tiles of 256 x
+// 256: a CTA alone reads 384 rows of operands per 128 x 256 products, a pair 256
+// rows per CTA, and operand reads from L2 (about 70 bytes per clock and SM) are
+// what bounds the product, not the tensor cores.
+template <class T, int BN, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     k_product(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, const Product p) {
-  constexpr int NST = stages(BN), SB = stage_bytes(BN), CW = chunk_cols(BN);
+  constexpr int NST = stages(BN, PAIR), SB = stage_bytes(BN, PAIR), CW = chunk_cols(BN), BR = b_rows(BN, PAIR);
+  constexpr int TM = PAIR ? 2 * kBM : kBM;  // rows of a tile
   extern __shared__ char raw[];
   char* base = reinterpret_cast<char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   char* patches = base + NST * SB;
@@ -239,6 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ unsigned dead, tmem_slot;
   const Guard g{&dead, p.error};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rank = PAIR ? (int)cluster_rank() : 0, first = PAIR ? blockIdx.x / 2 : blockIdx.x;
+  const int stride = PAIR ? gridDim.x / 2 : gridDim.x;
   if (threadIdx.x == 0) {
     dead = 0;
     for (int i = 0; i < NST; ++i) {
@@ -247,14 +258,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(accf + 8 * i, 1);
-      bar_init(acce + 8 * i, kEpiWarps);
+      bar_init(acce + 8 * i, PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     bar_init(drain, 1);
     bar_init_fence();
   }
-  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 2 * BN);
+  if (warp == 1) PAIR ? tmem_alloc_pair(smem_addr(&tmem_slot), 2 * BN) : tmem_alloc(smem_addr(&tmem_slot), 2 * BN);
   fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();  // barriers are ready in both CTAs
   fence_after();
   const uint32_t tmem = tmem_slot;
   const int items = p.tiles_m * p.tiles_n * p.splits;
@@ -266,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring<NST> r;
     unsigned issued = 0;
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
+    for (int w = first; ok && w < items; w += stride) {
       int tm, tn, k0, k1;
       work_item(p, w, &tm, &tn, &k0, &k1);
       for (int k = k0; k < k1; ++k) {
@@ -275,25 +287,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const uint32_t bar = full + 8 * r.slot, a = sm + r.slot * SB, b = a + kBM * kBK * 2;
-        bar_expect(bar, SB);
+        const uint32_t sig = PAIR ? cluster_addr(bar, 0) : bar;
+        const int am = tm * TM + rank * kBM, bn = tn * BN + rank * BR;
+        auto load = [&](uint32_t dst, const CUtensorMap* m, int x, int y) {
+          if (PAIR)
+            tma_load_2d_pair(dst, m, x, y, sig);
+          else
+            tma_load_2d(dst, m, x, y, sig);
+        };
+        if (rank == 0) bar_expect(bar, PAIR ? 2 * SB : SB);
         if (p.a_mn) {
 #pragma unroll
-          for (int i = 0; i < kBM / 64; ++i) tma_load_2d(a + i * 8192, &ma, tm * kBM + i * 64, k * kBK, bar);
+          for (int i = 0; i < kBM / 64; ++i) load(a + i * 8192, &ma, am + i * 64, k * kBK);
         } else {
-          tma_load_2d(a, &ma, k * kBK, tm * kBM, bar);
+          load(a, &ma, k * kBK, am);
         }
         if (p.b_mn) {
 #pragma unroll
-          for (int i = 0; i < BN / 64; ++i) tma_load_2d(b + i * 8192, &mb, tn * BN + i * 64, k * kBK, bar);
+          for (int i = 0; i < BR / 64; ++i) load(b + i * 8192, &mb, bn + i * 64, k * kBK);
         } else {
-          tma_load_2d(b, &mb, k * kBK, tn * BN, bar);
+          load(b, &mb, k * kBK, bn);
         }
         r.next();
         ++issued;
       }
     }
-    for (unsigned i = issued > NST ? issued - NST : 0; i < issued; ++i) bar_drain(full + 8 * (i % NST), (i / NST) & 1);
-  } else if (warp == 1 && elect_one()) {
+    // (the even CTA's barriers count the pair's copies; the odd one waits for it at the end)
+    if (rank == 0)
+      for (unsigned i = issued > NST ? issued - NST : 0; i < issued; ++i) bar_drain(full + 8 * (i % NST), (i / NST) & 1);
+  } else if (warp == 1 && rank == 0 && elect_one()) {
     Ring<NST> r;
     Ring<2> acc;
     bool ok = true;
@@ -301,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t a0 = (uint32_t)smem_desc(sm, 8192, 1024), b0 = (uint32_t)smem_desc(sm + kBM * kBK * 2, 8192, 1024);
     const uint32_t hi = (uint32_t)(smem_desc(0, 8192, 1024) >> 32);
     const uint32_t step_a = p.a_mn ? 128 : 2, step_b = p.b_mn ? 128 : 2;
-    for (int w = blockIdx.x; ok && w < items; w += gridDim.x) {
+    for (int w = first; ok && w < items; w += stride) {
       int tm, tn, k0, k1;
       work_item(p, w, &tm, &tn, &k0, &k1);
       if (!bar_wait(acce + 8 * acc.slot, acc.phase ^ 1u, g)) break;
@@ -315,30 +337,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_after();
         const uint32_t a = a0 + r.slot * (SB >> 4), b = b0 + r.slot * (SB >> 4);
-        mma_ss(d, a, hi, b, hi, p.idesc, add);
-        mma_ss(d, a + step_a, hi, b + step_b, hi, p.idesc, true);
-        mma_ss(d, a + 2 * step_a, hi, b + 2 * step_b, hi, p.idesc, true);
-        mma_ss(d, a + 3 * step_a, hi, b + 3 * step_b, hi, p.idesc, true);
-        mma_commit(empty + 8 * r.slot);
+#pragma unroll
+        for (int i = 0; i < kBK / 16; ++i) {
+          if (PAIR)
+            mma_ss_pair(d, a + i * step_a, hi, b + i * step_b, hi, p.idesc, add || i > 0);
+          else
+            mma_ss(d, a + i * step_a, hi, b + i * step_b, hi, p.idesc, add || i > 0);
+        }
+        PAIR ? mma_commit_pair(empty + 8 * r.slot) : mma_commit(empty + 8 * r.slot);
         add = true;
         r.next();
       }
-      mma_commit(accf + 8 * acc.slot);
+      PAIR ? mma_commit_pair(accf + 8 * acc.slot) : mma_commit(accf + 8 * acc.slot);
       acc.next();
     }
-    mma_commit(drain);
+    PAIR ? mma_commit_pair(drain) : mma_commit(drain);
     bar_drain(drain, 0);
   } else if (warp >= 4) {
     const int e = warp - 4, q = e % 4, half = e / 4;
     char* patch = patches + e * 32 * CW * 2;
     Ring<2> acc;
-    for (int w = blockIdx.x; w < items; w += gridDim.x) {
+    for (int w = first; w < items; w += stride) {
       int tm, tn, k0, k1;
       work_item(p, w, &tm, &tn, &k0, &k1);
       if (!bar_wait_warp(accf + 8 * acc.slot, acc.phase, g)) break;
       fence_after();
       const uint32_t d = tmem + acc.slot * BN + ((uint32_t)(q * 32) << 16);
-      const int m0 = tm * kBM + q * 32;
+      const int m0 = tm * TM + rank * kBM + q * 32;
 #pragma unroll 1
       for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += CW) {
         float v[CW];
@@ -353,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (c + CW == (half + 1) * (BN / 2)) {  // the last read of this accumulator
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive(acce + 8 * acc.slot);
+          if (lane == 0) PAIR && rank ? bar_arrive_remote(cluster_addr(acce + 8 * acc.slot, 0)) : bar_arrive(acce + 8 * acc.slot);
         }
         if (p.splits > 1) {
           float* o = p.partial + ((int64_t)w * BN + c) * kBM + q * 32 + lane;
@@ -368,7 +393,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 1) tmem_free(tmem, 2 * BN);
+  if (PAIR) {
+    // the odd CTA waits for the last arrival from the even one; then neither
+    // leaves while the other may use its memory
+    if (rank == 1 && threadIdx.x == 0) bar_drain(drain, 0);
+    __syncwarp();
+    cluster_sync();
+  }
+  if (warp == 1) PAIR ? tmem_free_pair(tmem, 2 * BN) : tmem_free(tmem, 2 * BN);
 }
 
 // Joins the partial products of a split contraction in order of the splits.
@@ -477,7 +509,7 @@ __global__ void __launch_bounds__(256) k_linear_gb(const LinearGradArgs a) {
   static_cast<T*>(a.gb)[n] = from_f32<T>(v);
 }
 
-template <class T, int BN>
+template <class T, int BN, bool PAIR>
 cudaError_t run_product(const CUtensorMap& ma, const CUtensorMap& mb, const Product& p, int grid, cudaStream_t s) {
   static std::atomic<unsigned long long> ready{0};  // one bit per device: shared-memory size granted
   int dev = 0;
@@ -485,13 +517,29 @@ cudaError_t run_product(const CUtensorMap& ma, const CUtensorMap& mb, const Prod
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(k_product<T, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(BN));
+    e = cudaFuncSetAttribute(k_product<T, BN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(BN, PAIR));
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
   note_launch_begin("k_product", s);
-  k_product<T, BN><<<grid, kThreads, smem_bytes(BN), s>>>(ma, mb, p);
+  if (PAIR) {
+    cudaLaunchConfig_t c{};
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.gridDim = dim3(2 * grid);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem_bytes(BN, PAIR);
+    c.stream = s;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    e = cudaLaunchKernelEx(&c, k_product<T, BN, PAIR>, ma, mb, p);
+  } else {
+    k_product<T, BN, PAIR><<<grid, kThreads, smem_bytes(BN, PAIR), s>>>(ma, mb, p);
+  }
   note_launch_end(s);
+  if (e != cudaSuccess) return e;
   if (p.splits > 1) {
     const int units = p.tiles_m * p.tiles_n * 4 * (BN / 32);
     note_launch_begin("k_product_join", s);
@@ -505,12 +553,19 @@ int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 }  // namespace
 
-// The tile is 128 x 256 where that gives every SM a tile (the least operand
+// Pairs of CTAs on tiles of 256 x 256 where those fill three quarters of the
+// pairs.  Else the tile is 128 x 256 where that gives every SM a tile (the least operand
 // traffic per product), else 128 x 128 or 128 x 64; a product with still fewer
 // tiles than SMs splits its contraction, at least 4 blocks of 64 per split.
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int sms) {
   LinearPlan l{};
   const int64_t tm = (M + kBM - 1) / kBM;
+  if (((M + 255) / 256) * ((N + 255) / 256) * 4 >= 3 * (sms / 2)) {
+    l.pair = 1;
+    l.bn = 256;
+    l.splits = 1;
+    return l;
+  }
   l.bn = 256;
   while (l.bn > 64 && tm * ((N + l.bn - 1) / l.bn) < sms) l.bn >>= 1;
   const int64_t tiles = tm * ((N + l.bn - 1) / l.bn), kb = (K + kBK - 1) / kBK;
@@ -531,7 +586,7 @@ cudaError_t launch_linear(int dt, const LinearArgs& a, int sms, float* partial, 
     return make_tensor_map(m, dt, ptr, 2, mn_major ? ext_mn : ext_k, &ld, mn_major ? box_m : box_k);
   };
   cudaError_t e = map(&ma, a.a, a.a_mn, a.lda, a.M, kBM);
-  if (e == cudaSuccess) e = map(&mb, a.b, a.b_mn, a.ldb, a.N, l.bn);
+  if (e == cudaSuccess) e = map(&mb, a.b, a.b_mn, a.ldb, a.N, b_rows(l.bn, l.pair));
   if (e != cudaSuccess) return e;
   Product p{};
   p.M = a.M;
@@ -539,11 +594,11 @@ cudaError_t launch_linear(int dt, const LinearArgs& a, int sms, float* partial, 
   p.K = a.K;
   p.a_mn = a.a_mn;
   p.b_mn = a.b_mn;
-  p.tiles_m = div_up(a.M, kBM);
+  p.tiles_m = div_up(a.M, l.pair ? 2 * kBM : kBM);
   p.tiles_n = div_up(a.N, l.bn);
   p.splits = l.splits;
   p.kb = div_up(a.K, kBK);
-  p.idesc = mma_idesc(dt == 2, a.a_mn, a.b_mn, kBM, l.bn);
+  p.idesc = mma_idesc(dt == 2, a.a_mn, a.b_mn, l.pair ? 2 * kBM : kBM, l.bn);
   p.c = a.c;
   p.ldc = a.ldc;
   p.bias = a.bias;
@@ -556,11 +611,12 @@ cudaError_t launch_linear(int dt, const LinearArgs& a, int sms, float* partial, 
   e = device_error_word(&p.error);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)p.tiles_m * p.tiles_n * p.splits;
-  const int grid = (int)(items < sms ? items : sms);
+  const int slots = l.pair ? sms / 2 : sms, grid = (int)(items < slots ? items : slots);
   FFDP_TOK_SWITCH16(dt, T, {
-    if (l.bn == 256) return run_product<T, 256>(ma, mb, p, grid, s);
-    if (l.bn == 128) return run_product<T, 128>(ma, mb, p, grid, s);
-    return run_product<T, 64>(ma, mb, p, grid, s);
+    if (l.pair) return run_product<T, 256, true>(ma, mb, p, grid, s);
+    if (l.bn == 256) return run_product<T, 256, false>(ma, mb, p, grid, s);
+    if (l.bn == 128) return run_product<T, 128, false>(ma, mb, p, grid, s);
+    return run_product<T, 64, false>(ma, mb, p, grid, s);
   });
 }
 
