@@ -83,14 +83,17 @@ template <> struct Pair<__nv_bfloat16> {
 };
 
 constexpr int kBM = 128, kBK = 64;
-constexpr int kThreads = 384;  // warp 0 loads, warp 1 multiplies, warps 4-11 run the epilogue
-constexpr int kEpiWarps = 8;
+// warp 0 loads, warp 1 multiplies, warps 4-19 run the epilogue, four per
+// scheduler: with two the GELU epilogue of 1024 products per output took longer
+// than the products
+constexpr int kThreads = 640;
+constexpr int kEpiWarps = 16;
 
 // Of a pair of CTAs each loads its half of B's rows (BN / 2).
 __host__ __device__ constexpr int b_rows(int BN, bool PAIR) { return PAIR ? BN / 2 : BN; }
 __host__ __device__ constexpr int stages(int BN, bool PAIR) { return BN == 256 && !PAIR ? 4 : 6; }
 __host__ __device__ constexpr int stage_bytes(int BN, bool PAIR) { return (kBM + b_rows(BN, PAIR)) * kBK * 2; }
-__host__ __device__ constexpr int chunk_cols(int BN) { return BN / 2 < 64 ? BN / 2 : 64; }
+__host__ __device__ constexpr int chunk_cols(int BN) { return BN / 4 < 32 ? BN / 4 : 32; }
 __host__ __device__ constexpr int stage_out_bytes(int BN) { return kEpiWarps * 32 * chunk_cols(BN) * 2; }
 constexpr size_t smem_bytes(int BN, bool PAIR) {
   return 1024 + (size_t)stages(BN, PAIR) * stage_bytes(BN, PAIR) + stage_out_bytes(BN) + 256;
@@ -132,7 +135,7 @@ __device__ __forceinline__ void work_item(const Product& p, int w, int* tm, int*
 template <class T, int CW>
 __device__ __forceinline__ void finish(const Product& p, float* v, int m0, int n0, char* patch, int lane) {
   constexpr int CH = CW / 8, RP = 32 / CH;  // 16-byte pieces per row, rows per access
-  auto at = [&](int row, int piece) { return reinterpret_cast<uint4*>(patch + row * CW * 2 + ((piece ^ (row % CH)) * 16)); };
+  auto at = [&](int row, int piece) { return reinterpret_cast<uint4*>(patch + row * CW * 2 + ((piece ^ (row * CH / 8 % CH)) * 16)); };
   const int rows = min(32, p.M - m0);
   auto flush = [&](void* out, int64_t ld) {
     __syncwarp();
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     PAIR ? mma_commit_pair(drain) : mma_commit(drain);
     bar_drain(drain, 0);
   } else if (warp >= 4) {
-    const int e = warp - 4, q = e % 4, half = e / 4;
+    const int e = warp - 4, q = e % 4, part = e / 4;
     char* patch = patches + e * 32 * CW * 2;
     Ring<2> acc;
     for (int w = first; w < items; w += stride) {
@@ -365,17 +368,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d = tmem + acc.slot * BN + ((uint32_t)(q * 32) << 16);
       const int m0 = tm * TM + rank * kBM + q * 32;
 #pragma unroll 1
-      for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += CW) {
+      for (int c = part * (BN / 4); c < (part + 1) * (BN / 4); c += CW) {
         float v[CW];
         if (k1 > k0) {
-#pragma unroll
-          for (int i = 0; i < CW; i += 32) tmem_ld32(d + c + i, v + i);
+          CW == 32 ? tmem_ld32(d + c, v) : tmem_ld16(d + c, v);
           tmem_wait_ld();
         } else {
 #pragma unroll
           for (int i = 0; i < CW; ++i) v[i] = 0.0f;
         }
-        if (c + CW == (half + 1) * (BN / 2)) {  // the last read of this accumulator
+        if (c + CW == (part + 1) * (BN / 4)) {  // the last read of this accumulator
           fence_before();
           __syncwarp();
           if (lane == 0) PAIR && rank ? bar_arrive_remote(cluster_addr(acce + 8 * acc.slot, 0)) : bar_arrive(acce + 8 * acc.slot);
