@@ -181,15 +181,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int prefix = prefix_of(a, x.b), buf = k & 1;
         if (!(ok = bar_wait_warp(pfree + 8 * buf, ((k >> 1) & 1u) ^ 1u, guard))) break;
         int count = 0;
+        // from the key tile beside the queries on, and around: with a distance
+        // bias the row maxima hardly move after the first tile
+        const int start = min(max((x.i0[0] + max(0, a.Sk - a.Sq)) / kTile - x.j0, 0), x.n - 1);
         for (int j = 0; j < x.n; j += 32) {
           int code = 0;
+          const int at = j + lane + start < x.n ? j + lane + start : j + lane + start - x.n;
           if (j + lane < x.n) {
-            const int y0 = (x.j0 + j + lane) * kTile;
+            const int y0 = (x.j0 + at) * kTile;
             code = pair_code(a, prefix, x.b, x.i0[0], x.i1[0], y0, y0 + kTile, f.dq, f.dk) |
                    pair_code(a, prefix, x.b, x.i0[1], x.i1[1], y0, y0 + kTile, f.dq, f.dk) << 2;
           }
           const unsigned seen = __ballot_sync(0xffffffffu, code != 0);
-          if (code) plan[buf][count + __popc(seen & ((1u << lane) - 1u))] = (uint16_t)((j + lane) | code << 11);
+          if (code) plan[buf][count + __popc(seen & ((1u << lane) - 1u))] = (uint16_t)(at | code << 11);
           count += __popc(seen);
         }
         if (lane == 0) planned[buf] = count;
