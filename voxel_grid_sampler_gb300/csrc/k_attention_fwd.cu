@@ -517,20 +517,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (++slot == NS) slot = 0, phase ^= 1u;
             continue;
           }
-          f32x2 v[4][16];  // rows by pairs of keys
-          {
-            float s[128];
-            tmem_ld_frag16(s_at(t) + lanes, s);
-            tmem_ld_frag16(s_at(t) + lanes + (16u << 16), s + 64);
-            tmem_wait_ld();
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-#pragma unroll
-              for (int g = 0; g < 16; ++g) {
-                const int at = (y / 2) * 64 + 4 * g + (y % 2) * 2;
-                v[y][g] = pair(s[at], s[at + 1]);
-              }
-          }
+          float s[128];  // row y, keys 8 g + cb and + 1: at(y, g) and + 1
+          auto at = [](int y, int g) { return (y / 2) * 64 + 4 * g + (y % 2) * 2; };
+          tmem_ld_frag16(s_at(t) + lanes, s);
+          tmem_ld_frag16(s_at(t) + lanes + (16u << 16), s + 64);
+          tmem_wait_ld();
           if (own_p) {  // the next S may be computed meanwhile
             fence_before();
             __syncwarp();
@@ -544,8 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int y = 0; y < 4; ++y)
 #pragma unroll
               for (int g = 0; g < 16; ++g) {
-                const float2 z = split(mul2(v[y][g], in));
-                v[y][g] = fma2(out, pair(rcp(1.0f + ex2(z.x)), rcp(1.0f + ex2(z.y))), cap);
+                float* w = s + at(y, g);
+                const float2 z = split(mul2(pair(w[0], w[1]), in));
+                const float2 c = split(fma2(out, pair(rcp(1.0f + ex2(z.x)), rcp(1.0f + ex2(z.y))), cap));
+                w[0] = c.x, w[1] = c.y;
               }
           }
           float shift[4] = {};  // of whole rows
@@ -555,7 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int y = 0; y < 4; ++y)
 #pragma unroll
-              for (int g = 0; g < 16; ++g) v[y][g] = mul2(v[y][g], sc2);
+              for (int g = 0; g < 16; ++g) {
+                float* w = s + at(y, g);
+                const float2 c = split(mul2(pair(w[0], w[1]), sc2));
+                w[0] = c.x, w[1] = c.y;
+              }
 #pragma unroll 1
             for (int ax = 0; ax < a.axes; ++ax) {
               const float* kp = x.pos[0][ax] + cb;
@@ -571,7 +568,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int g = 0; g < 16; ++g) {
                 const f32x2 kk = *reinterpret_cast<const f32x2*>(kp + 8 * g);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) v[y][g] = fma2(neg_abs2(add2(kk, np[y])), q[y], v[y][g]);
+                for (int y = 0; y < 4; ++y) {
+                  float* w = s + at(y, g);
+                  const float2 c = split(fma2(neg_abs2(add2(kk, np[y])), q[y], pair(w[0], w[1])));
+                  w[0] = c.x, w[1] = c.y;
+                }
               }
             }
           } else if (AXES) {
@@ -581,26 +582,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int g = 0; g < 16; ++g) {
               const f32x2 kk = *reinterpret_cast<const f32x2*>(kf + 8 * g);
 #pragma unroll
-              for (int y = 0; y < 4; ++y) v[y][g] = fma2(v[y][g], sc2, kk);
+              for (int y = 0; y < 4; ++y) {
+                float* w = s + at(y, g);
+                const float2 c = split(fma2(pair(w[0], w[1]), sc2, kk));
+                w[0] = c.x, w[1] = c.y;
+              }
             }
 #pragma unroll 1
             for (int ax = 0; ax < 3; ++ax) {
               const float side = x.side[t][ax];
-              f32x2 np[4];
+              float p[4];
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                const float p = rowpos[t][ax][r0 + 8 * y];
-                shift[y] = fmaf(side, p, shift[y]);
-                np[y] = pair(-p, -p);
+                p[y] = rowpos[t][ax][r0 + 8 * y];
+                shift[y] = fmaf(side, p[y], shift[y]);
               }
               if (side != 0.0f) continue;
               const float* kp = x.pos[t][ax] + cb;
+              // scalar: an addition takes |d| for free, a pair of them does not
 #pragma unroll
               for (int g = 0; g < 16; ++g) {
-                const f32x2 kk = *reinterpret_cast<const f32x2*>(kp + 8 * g);
+                const float2 kk = *reinterpret_cast<const float2*>(kp + 8 * g);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                  v[y][g] = add2(v[y][g], neg_abs2(add2(kk, np[y])));
+                  float* w = s + at(y, g);
+                  w[0] -= fabsf(kk.x - p[y]);
+                  w[1] -= fabsf(kk.y - p[y]);
                 }
               }
             }
@@ -614,8 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int left = rowlimit[t][r0 + 8 * y] - key0 - cb;  // keys before the limit, from this thread's first on
 #pragma unroll
                 for (int g = 0; g < 16; ++g) {
-                  const float2 z = split(v[y][g]);
-                  v[y][g] = pair(8 * g < left ? z.x : -INFINITY, 8 * g + 1 < left ? z.y : -INFINITY);
+                  float* w = s + at(y, g);
+                  w[0] = 8 * g < left ? w[0] : -INFINITY;
+                  w[1] = 8 * g + 1 < left ? w[1] : -INFINITY;
                 }
               }
             }
@@ -628,8 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int2 d = *reinterpret_cast<const int2*>(x.doc + 8 * g + cb);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                  const float2 z = split(v[y][g]);
-                  v[y][g] = pair(d.x == dq[y] ? z.x : -INFINITY, d.y == dq[y] ? z.y : -INFINITY);
+                  float* w = s + at(y, g);
+                  w[0] = d.x == dq[y] ? w[0] : -INFINITY;
+                  w[1] = d.y == dq[y] ? w[1] : -INFINITY;
                 }
               }
             }
@@ -641,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < kTile; ++c)
                   if ((x.bad[c / 32] >> (c % 32)) & 1u) poison |= key0 + c < limit && (!a.doc_q || x.doc[c] == dq);
-                if (poison) v[y][0] = pair(NAN, NAN);
+                if (poison) s[at(y, 0)] = NAN;
               }
             }
           }
@@ -652,8 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int g = 0; g < 16; ++g) {
-              const float2 z = split(v[y][g]);
-              mx[g % 2] = max3(mx[g % 2], z.x, z.y);
+              const float* w = s + at(y, g);
+              mx[g % 2] = max3(mx[g % 2], w[0], w[1]);
             }
             top[y] = fmaxf(mx[0], mx[1]);
           }
@@ -711,7 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int g = 0; g < 8; ++g)
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
-                const f32x2 z = v[y0 + y][q % 2 * 8 + g];
+                const float* w = s + at(y0 + y, q % 2 * 8 + g);
+                const f32x2 z = pair(w[0], w[1]);
                 const float2 d = split(CAP || AXES ? add2(z, mm[y0 + y]) : fma2(z, c22, mm[y0 + y]));
                 const float p0 = ex2(d.x), p1 = ex2(d.y);
                 sum[y0 + y] = add2(sum[y0 + y], pair(p0, p1));
