@@ -256,3 +256,26 @@ def test_gradients_against_differences(ffdp, cap, causal):
         num = float((f(1e-4) - f(-1e-4)) / 2e-4)
         bound = float((want["g" + n][1] * e.abs()).sum()) + 1e-6 * abs(num)
         assert abs(float((ref.d(g) * e).sum()) - num) <= bound, n
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+@pytest.mark.parametrize("Sq", [2, 150])
+def test_negative_and_zero_scale(ffdp, scale, Sq):
+    t, more = _inputs(22, 2, Sq, 200, 4, 2, 64, BF16, axes=2, docs=2)
+    _check(ffdp, t, more, scale=scale)
+    _check(ffdp, t, more, scale=scale, cap=1.5)
+
+
+@pytest.mark.parametrize("Sq,Hq", [(130, 1), (1, 8), (12, 2)])
+def test_very_long_keys(ffdp, Sq, Hq):
+    # more key tiles than one work item lists, and than a backward CTA keeps codes for
+    t, more = _inputs(23, 1, Sq, 270001, Hq, 1, 32, F16, axes=1)
+    more["slopes"] *= 0.01
+    _check(ffdp, t, more, causal=True, train=Sq == 12)
+
+
+@pytest.mark.parametrize("G,Sq", [(1, 16), (4, 4), (16, 1), (17, 1), (3, 21), (128, 1), (5, 64)])
+def test_few_rows_in_every_packing(ffdp, G, Sq):
+    # 16 rows per key head, just above, tiles of several heads that fill 128 rows or do not
+    t, more = _inputs(24, 2, Sq, 333, 2 * G, 2, 72, BF16, axes=3, docs=2)
+    _check(ffdp, t, more, train=G < 16, causal=True, cap=10.0)
