@@ -81,8 +81,8 @@ struct FewArgs {
 };
 int few_splits(int64_t pairs, int64_t keys, int sms);
 cudaError_t launch_attention_few(int dt, const AttnArgs& a, const FewArgs& f, cudaStream_t s);
-size_t attention_bwd_bytes(const AttnArgs& a);
-cudaError_t launch_attention_bwd(int dt, const AttnArgs& a, void* ws, cudaStream_t s);
+size_t attention_bwd_bytes(const AttnArgs& a, int sms);
+cudaError_t launch_attention_bwd(int dt, const AttnArgs& a, int sms, void* ws, cudaStream_t s);
 
 // C[m][n] = sum_k A(m, k) B(n, k).  An operand is K-major (rows m or n of K
 // elements) or MN-major (rows k of M or N elements), rows ld elements apart.

@@ -200,7 +200,7 @@ size_t attention_ws(const ffdp_attention_params* p, int backward) {
     const AttnPlan l = attention_plan(a, sms());
     return 256 + l.ranges_bytes + l.part_bytes;
   }
-  return 256 + attention_bwd_bytes(a);
+  return 256 + attention_bwd_bytes(a, sms());
 }
 
 }  // namespace
@@ -254,7 +254,7 @@ extern "C" ffdp_status ffdp_attention_bwd(const ffdp_heads* q, const ffdp_heads*
   TRY(check_ws(ws, ws_bytes, attention_ws(p, 1)));
   a.lse = const_cast<float*>(lse);
   if (a.B == 0) return FFDP_OK;
-  LAUNCH(launch_attention_bwd(dt, a, ws, static_cast<cudaStream_t>(stream)), "attention backward launch");
+  LAUNCH(launch_attention_bwd(dt, a, sms(), ws, static_cast<cudaStream_t>(stream)), "attention backward launch");
   return FFDP_OK;
 }
 

@@ -37,6 +37,7 @@ struct BwdArgs {
   uint32_t idesc_s, idesc_dp, idesc_acc;
   float c;             // |scale| log2 e
   float cap_in, cap2;  // 2 log2 e |scale| / cap, cap log2 e
+  float* part;         // keys resident, one query head per CTA: [gv, gk][B][Hq][Sk][D], or NULL
   unsigned* error;
 };
 
@@ -67,7 +68,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   // this CTA's resident tile; causal calls begin with the longest walks
-  const int H = KV ? a.Hk : a.Hq, tiles = ((KV ? a.Sk : a.Sq) + kTile - 1) / kTile;
+  const bool by_head = KV && f.part;  // a query head per CTA, not a key head
+  const int H = KV && !by_head ? a.Hk : a.Hq, tiles = ((KV ? a.Sk : a.Sq) + kTile - 1) / kTile;
   int tile, bh;
   if (a.causal) {
     tile = blockIdx.x / (a.B * H);
@@ -77,9 +79,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bh = blockIdx.x / tiles;
     tile = blockIdx.x - bh * tiles;
   }
-  const int b = bh / H, hr = bh - b * H;          // resident head
-  const int g = KV ? hr : hr / a.G;               // key head
-  const int heads = KV ? a.G : 1, h0 = KV ? hr * a.G : hr;  // query heads walked
+  const int b = bh / H, hx = bh - b * H;
+  const int g = KV && !by_head ? hx : hx / a.G;   // key head
+  const int hr = KV ? g : hx;                     // resident head
+  const int heads = KV && !by_head ? a.G : 1, h0 = KV && !by_head ? g * a.G : hx;  // query heads walked
   const int prefix = prefix_of(a, b);
   const int x0 = tile * kTile, x1 = min(x0 + kTile, KV ? a.Sk : a.Sq);
   const int walk = KV ? a.Sq : a.Sk, nsub = (walk + kSub - 1) / kSub;
@@ -416,6 +419,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = 0.0f;
       }
+      if (by_head) {
+        float* p = f.part + ((((int64_t)wg * a.B + b) * a.Hq + h0) * a.Sk + xc) * a.D + c;
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          if (valid && c + e < a.D) *reinterpret_cast<float4*>(p + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        __syncwarp();
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < 32; e += 8)
         if (valid && c + e < a.D)
@@ -429,6 +440,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   if (warp == 9) tmem_free(tmem, kTmemCols);
+}
+
+// gv and gk from the query heads' parts, in the order of the heads; four
+// channels per thread.
+template <class T>
+__global__ void __launch_bounds__(256) k_attn_heads(const BwdArgs f) {
+  const AttnArgs& a = f.a;
+  const int quads = a.D / 4;
+  const int64_t n = (int64_t)a.B * a.Hk * a.Sk * quads, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= 2 * n) return;
+  const int which = i >= n;  // 0: gv, 1: gk
+  int64_t r = i - which * n;
+  const int c = (int)(r % quads) * 4;
+  r /= quads;
+  const int j = (int)(r % a.Sk), g = (int)(r / a.Sk % a.Hk), b = (int)(r / a.Sk / a.Hk);
+  const float* p = f.part + ((((int64_t)which * a.B + b) * a.Hq + g * a.G) * a.Sk + j) * a.D + c;
+  float4 t = *reinterpret_cast<const float4*>(p);
+  for (int h = 1; h < a.G; ++h) {
+    const float4 u = *reinterpret_cast<const float4*>(p + (int64_t)h * a.Sk * a.D);
+    t.x += u.x, t.y += u.y, t.z += u.z, t.w += u.w;
+  }
+  const HeadsView& v = which ? a.gk : a.gv;
+  T* o = static_cast<T*>(v.p) + b * v.sb + (int64_t)j * v.st + g * v.sh + c;
+  *reinterpret_cast<uint2*>(o) = make_uint2(pack2<T>(t.x, t.y), pack2<T>(t.z, t.w));
 }
 
 // delta = sum_d go o, 16 lanes per row.
@@ -469,7 +504,7 @@ cudaError_t run(const CUtensorMap* m, const BwdArgs& f, cudaStream_t s) {
   }
   const int64_t tiles = ((KV ? f.a.Sk : f.a.Sq) + kTile - 1) / kTile;
   note_launch_begin(KV ? "k_attn_bwd_kv" : "k_attn_bwd_q", s);
-  k_attn_bwd<T, AXES, CAP, KV><<<(unsigned)(tiles * f.a.B * (KV ? f.a.Hk : f.a.Hq)), kThreads, smem, s>>>(m[0], m[1], m[2], m[3], f);
+  k_attn_bwd<T, AXES, CAP, KV><<<(unsigned)(tiles * f.a.B * (KV && !f.part ? f.a.Hk : f.a.Hq)), kThreads, smem, s>>>(m[0], m[1], m[2], m[3], f);
   note_launch_end(s);
   return cudaGetLastError();
 }
@@ -484,22 +519,41 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
-size_t attention_bwd_bytes(const AttnArgs& a) {
-  return round256((size_t)a.B * a.Hq * a.Sq * 4) + round256((size_t)a.B * ((a.Sq + kTile - 1) / kTile) * sizeof(DocRange)) +
-         round256((size_t)a.B * ((a.Sk + kTile - 1) / kTile) * sizeof(DocRange));
+namespace {
+
+// Keys resident, a CTA walks all query heads of a key head; where that leaves
+// fewer than four CTAs per SM, one query head each, their parts summed after: the
+// parts' traffic (8 bytes per element, twice) costs less than the last wave's
+// idle SMs and the longest document's lone CTA (2 x 4096 tokens in five
+// documents, 16 / 4 heads of 128: 438 us by key head).
+bool heads_apart(const AttnArgs& a, int sms) {
+  return a.G > 1 && (int64_t)a.B * a.Hk * ((a.Sk + kTile - 1) / kTile) < 4 * (int64_t)sms;
+}
+size_t part_bytes(const AttnArgs& a, int sms) {
+  return heads_apart(a, sms) ? round256((size_t)2 * a.B * a.Hq * a.Sk * a.D * 4) : 0;
 }
 
-cudaError_t launch_attention_bwd(int dt, const AttnArgs& args, void* ws, cudaStream_t s) {
+}  // namespace
+
+size_t attention_bwd_bytes(const AttnArgs& a, int sms) {
+  return round256((size_t)a.B * a.Hq * a.Sq * 4) + round256((size_t)a.B * ((a.Sq + kTile - 1) / kTile) * sizeof(DocRange)) +
+         round256((size_t)a.B * ((a.Sk + kTile - 1) / kTile) * sizeof(DocRange)) + part_bytes(a, sms);
+}
+
+cudaError_t launch_attention_bwd(int dt, const AttnArgs& args, int sms, void* ws, cudaStream_t s) {
   BwdArgs f{};
   f.a = args;
   AttnArgs& a = f.a;
   char* w = static_cast<char*>(ws);
   a.delta = reinterpret_cast<float*>(w);
   w += round256((size_t)a.B * a.Hq * a.Sq * 4);
+  DocRange* dq = reinterpret_cast<DocRange*>(w);
+  w += round256((size_t)a.B * ((a.Sq + kTile - 1) / kTile) * sizeof(DocRange));
+  DocRange* dk = reinterpret_cast<DocRange*>(w);
+  w += round256((size_t)a.B * ((a.Sk + kTile - 1) / kTile) * sizeof(DocRange));
+  if (heads_apart(a, sms)) f.part = reinterpret_cast<float*>(w);
   cudaError_t e = cudaSuccess;
   if (a.doc_q) {
-    DocRange* dq = reinterpret_cast<DocRange*>(w);
-    DocRange* dk = reinterpret_cast<DocRange*>(w + round256((size_t)a.B * ((a.Sq + kTile - 1) / kTile) * sizeof(DocRange)));
     e = launch_doc_ranges(a, dq, dk, s);
     f.dq = dq;
     f.dk = dk;
@@ -537,6 +591,13 @@ cudaError_t launch_attention_bwd(int dt, const AttnArgs& args, void* ws, cudaStr
     if (e != cudaSuccess) return e;
     FFDP_TOK_SWITCH16(dt, T, { e = kv ? pick<T, true>(m, f, s) : pick<T, false>(m, f, s); });
     if (e != cudaSuccess) return e;
+    if (kv && f.part) {
+      const int64_t threads = 2 * (int64_t)a.B * a.Hk * a.Sk * (a.D / 4);
+      note_launch_begin("k_attn_heads", s);
+      FFDP_TOK_SWITCH16(dt, T, (k_attn_heads<T><<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(f)));
+      note_launch_end(s);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
   }
   return cudaSuccess;
 }
