@@ -10,7 +10,7 @@ namespace ffdp {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 // VEC elements of T as one aligned load / store (VEC * sizeof(T) <= 16 bytes).
 template <class T, int VEC>
@@ -100,10 +100,11 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeArgs a, int tok
 
 template <class T, int VEC>
 cudaError_t run(bool inter, const RopeArgs& a, cudaStream_t s) {
-  // 8 tokens per CTA: about one sine and cosine per thread at 32 pairs, and
-  // several independent 16-byte loads per thread in flight; fewer where the
+  // 4 tokens per CTA of 128 threads: about one sine and cosine per thread at 32 pairs,
+  // several independent 16-byte loads per thread in flight (256 threads and 8 tokens:
+  // 47.6 us for 220 MB, this: 43.5, launch included); fewer where the
   // table would pass 32 KB
-  int tokens = 8;
+  int tokens = 4;
   while (tokens > 1 && tokens * a.R * (int)sizeof(float2) > 32768) tokens >>= 1;
   const int grid = (a.B * a.S + tokens - 1) / tokens;
   const size_t smem = (size_t)tokens * a.R * sizeof(float2);
