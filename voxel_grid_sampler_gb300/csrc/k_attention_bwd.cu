@@ -28,6 +28,7 @@ constexpr int kThreads = 384;
 constexpr int kSub = 64;                // walked tokens per step
 constexpr int kSubPanel = kSub * 128;   // bytes of 64 channels of a subtile
 constexpr int kStages = 4;
+constexpr int kChunk = 16;              // walked tokens that a thread turns at a time
 constexpr unsigned kTmemCols = 512;
 
 struct BwdArgs {
@@ -306,13 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after();
       const Aux& u = aux[r.slot];
 #pragma unroll 1
-      for (int c0 = 0; c0 < kSub; c0 += 32) {
-        float s[32], d[32];
-        tmem_ld32(s_at(wg) + lanes + c0, s);
-        tmem_ld32(dp_at(wg) + lanes + c0, d);
+      for (int c0 = 0; c0 < kSub; c0 += kChunk) {
+        float s[kChunk], d[kChunk];
+        tmem_ld16(s_at(wg) + lanes + c0, s);
+        tmem_ld16(dp_at(wg) + lanes + c0, d);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
+        for (int c = 0; c < kChunk; c += 4) {
           const float4 lse = KV ? *reinterpret_cast<const float4*>(u.lse + c0 + c) : make_float4(lse_r, lse_r, lse_r, lse_r);
           const float4 del = KV ? *reinterpret_cast<const float4*>(u.delta + c0 + c) : make_float4(delta_r, delta_r, delta_r, delta_r);
           const float ls[4] = {lse.x, lse.y, lse.z, lse.w}, de[4] = {del.x, del.y, del.z, del.w};
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (cur.code == kMasked) {
           if (KV && a.causal) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
+            for (int c = 0; c < kChunk; c += 4) {
               const int4 q = *reinterpret_cast<const int4*>(u.limit + c0 + c);
               const int lim[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -358,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (!KV) {
             const int left = limit - cur.n * kSub - c0;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) d[c] = c < left ? d[c] : 0.0f;
+            for (int c = 0; c < kChunk; ++c) d[c] = c < left ? d[c] : 0.0f;
           }
           if (a.doc_q) {
 #pragma unroll
-            for (int c = 0; c < 32; c += 4) {
+            for (int c = 0; c < kChunk; c += 4) {
               const int4 q = *reinterpret_cast<const int4*>(u.doc + c0 + c);
               const int dc[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -372,11 +373,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const unsigned bad = u.bad[c0 / 32];
+          const unsigned bad = (u.bad[c0 / 32] >> (c0 % 32)) & ((1u << kChunk) - 1u);
           if (bad) {  // a visible non-finite row makes this thread's results NaN
             bool poison = false;
 #pragma unroll 1
-            for (int c = 0; c < 32; ++c) {
+            for (int c = 0; c < kChunk; ++c) {
               if (!((bad >> c) & 1u)) continue;
               bool see = KV ? !a.causal || x < u.limit[c0 + c] : cur.n * kSub + c0 + c < limit;
               if (a.doc_q) see = see && doc == u.doc[c0 + c];
@@ -385,15 +386,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (poison) s[0] = d[0] = NAN;
           }
         }
-        uint32_t w[16];
+        uint32_t w[kChunk / 2];
         if (KV) {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) w[c] = pack2<T>(s[2 * c], s[2 * c + 1]);
-          tmem_st16(s_at(wg) + lanes + c0 / 2, w);
+          for (int c = 0; c < kChunk / 2; ++c) w[c] = pack2<T>(s[2 * c], s[2 * c + 1]);
+          tmem_st8(s_at(wg) + lanes + c0 / 2, w);
         }
 #pragma unroll
-        for (int c = 0; c < 16; ++c) w[c] = pack2<T>(d[2 * c], d[2 * c + 1]);
-        tmem_st16(dp_at(wg) + lanes + c0 / 2, w);
+        for (int c = 0; c < kChunk / 2; ++c) w[c] = pack2<T>(d[2 * c], d[2 * c + 1]);
+        tmem_st8(dp_at(wg) + lanes + c0 / 2, w);
       }
       tmem_wait_st();
       fence_before();
