@@ -9,11 +9,12 @@
 // 32-bit gradient buffer, for two of seven products done twice.
 //
 // Walked tokens come in subtiles of 64, two in flight: S = R1 T1^T and dP = R2
-// T2^T (R: resident rows, T: walked rows) go to TMEM, a warpgroup per subtile
-// (one resident row per thread) turns them into P and dS in 16 bits in the
-// same columns, which are the A operands of the accumulating products.  Warps:
-// 0-3 and 4-7 even and odd subtiles, 8 loads (TMA), 9 multiplies, 10 and 11
-// prepare each subtile's lse, delta, positions, documents and non-finite rows.
+// T2^T (R: resident rows, T: walked rows) go to TMEM, two warpgroups per
+// subtile (a thread has one resident row and half of the walked tokens) turn them
+// into P and dS in 16 bits in the same columns, which are the A operands of the
+// accumulating products.  Warps: 0-7 and 8-15 even and odd subtiles, 16 loads
+// (TMA), 17 multiplies, 18 and 19 prepare each subtile's lse, delta, positions,
+// documents and non-finite rows.
 #include <atomic>
 
 #include "ffdp_attention.cuh"
@@ -24,7 +25,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kSub = 64;                // walked tokens per step
 constexpr int kSubPanel = kSub * 128;   // bytes of 64 channels of a subtile
 constexpr int kStages = 4;
@@ -103,14 +104,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       bar_init(sfull + 8 * s, 1);
-      bar_init(pfull + 8 * s, 4);
+      bar_init(pfull + 8 * s, 8);
       bar_init(done + 8 * s, 1);
     }
     bar_init(accfull, 1);
     bar_init(drain, 1);
     bar_init_fence();
   }
-  if (warp == 9) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
+  if (warp == 17) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
   fence_before();
   __syncthreads();
   fence_after();
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   Step cur = advance(Step{nsub > 0 ? 0 : heads, 0, 0});
 
-  if (warp == 8 && elect_one()) {
+  if (warp == 16 && elect_one()) {
     if (cur.head < heads) {
       bar_expect(rfull, 2 * res_bytes);
       for (int p = 0; p < f.panels; ++p) {
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (unsigned i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
         bar_drain(tfull + 8 * (i % kStages), (i / kStages) & 1);
     }
-  } else if (warp == 9 && elect_one()) {
+  } else if (warp == 17 && elect_one()) {
     const int ksteps = (a.D + 15) / 16;
     Ring<kStages> ts, ta;       // slots of the scores' and of the accumulating products
     unsigned n = 0;             // subtiles whose scores were issued
@@ -208,8 +209,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t t = smem_addr(st + ta.slot * 2 * sub_bytes);
 #pragma unroll
       for (int k = 0; k < kSub / 16; ++k) {
-        if (KV) mma_ts(acc1, s_at(s) + k * 8, smem_desc(t + sub_bytes + k * 2048, kSubPanel, 1024), f.idesc_acc, m > 0 || k > 0);
-        mma_ts(acc2, dp_at(s) + k * 8, smem_desc(t + k * 2048, kSubPanel, 1024), f.idesc_acc, m > 0 || k > 0);
+        if (KV) mma_ts(acc1, s_at(s) + k / 2 * 32 + k % 2 * 8, smem_desc(t + sub_bytes + k * 2048, kSubPanel, 1024), f.idesc_acc, m > 0 || k > 0);
+        mma_ts(acc2, dp_at(s) + k / 2 * 32 + k % 2 * 8, smem_desc(t + k * 2048, kSubPanel, 1024), f.idesc_acc, m > 0 || k > 0);
       }
       mma_commit(done + 8 * s);
       mma_commit(tempty + 8 * ta.slot);
@@ -219,9 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit(accfull);
     mma_commit(drain);
     bar_drain(drain, 0);
-  } else if (warp >= 10) {
+  } else if (warp >= 18) {
     Ring<kStages> r;
-    const int e = (warp - 10) * 32 + lane;  // token of the subtile
+    const int e = (warp - 18) * 32 + lane;  // token of the subtile
     const bool hide = a.causal || a.doc_q;  // past the last token a subtile holds zeros anyway
     for (; cur.head < heads; cur = next(cur)) {
       const int h = h0 + cur.head, y = cur.n * kSub + e;
@@ -263,14 +264,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
         }
         const unsigned m = __ballot_sync(0xffffffffu, bad);
-        if (lane == 0) x.bad[warp - 10] = m;
+        if (lane == 0) x.bad[warp - 18] = m;
       }
       __syncwarp();
       if (lane == 0) bar_arrive(ready + 8 * r.slot);
       r.next();
     }
-  } else if (warp < 8) {
-    const int wg = warp / 4, row = (warp % 4) * 32 + lane, x = x0 + row;
+  } else if (warp < 16) {
+    const int wg = warp / 8, half = warp / 4 % 2, row = (warp % 4) * 32 + lane, x = x0 + row;
     const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
     const bool valid = x < x1;
     const int xc = valid ? x : x0;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after();
       const Aux& u = aux[r.slot];
 #pragma unroll 1
-      for (int c0 = 0; c0 < kSub; c0 += kChunk) {
+      for (int c0 = half * (kSub / 2); c0 < (half + 1) * (kSub / 2); c0 += kChunk) {
         float s[kChunk], d[kChunk];
         tmem_ld16(s_at(wg) + lanes + c0, s);
         tmem_ld16(dp_at(wg) + lanes + c0, d);
@@ -386,15 +387,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (poison) s[0] = d[0] = NAN;
           }
         }
+        const int p_col = 32 * half + (c0 - 32 * half) / 2;  // in this half's own columns, which it has read
         uint32_t w[kChunk / 2];
         if (KV) {
 #pragma unroll
           for (int c = 0; c < kChunk / 2; ++c) w[c] = pack2<T>(s[2 * c], s[2 * c + 1]);
-          tmem_st8(s_at(wg) + lanes + c0 / 2, w);
+          tmem_st8(s_at(wg) + lanes + p_col, w);
         }
 #pragma unroll
         for (int c = 0; c < kChunk / 2; ++c) w[c] = pack2<T>(d[2 * c], d[2 * c + 1]);
-        tmem_st8(dp_at(wg) + lanes + c0 / 2, w);
+        tmem_st8(dp_at(wg) + lanes + p_col, w);
       }
       tmem_wait_st();
       fence_before();
@@ -403,13 +405,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     ok = ok && bar_wait_warp(accfull, 0, guard);
     fence_after();
-    // keys resident: gv from the first warpgroup, gk from the second; queries:
-    // half of gq's channels each
+    // keys resident: gv from the even subtiles' warps, gk from the odd ones',
+    // each half of the channels; queries: a quarter of gq's channels each
     const HeadsView& out = KV ? (wg == 0 ? a.gv : a.gk) : a.gq;
     const uint32_t acc = KV && wg == 0 ? acc1 : acc2;
     const float scale = KV && wg == 0 ? 1.0f : a.scale;
     T* o = static_cast<T*>(out.p) + b * out.sb + (int64_t)xc * out.st + hr * out.sh;
-    for (int c = KV ? 0 : 32 * wg; c < a.D; c += KV ? 32 : 64) {
+    for (int c = KV ? 32 * half : 32 * (2 * wg + half); c < a.D; c += KV ? 64 : 128) {
       float v[32];
       if (ok && n) {
         tmem_ld32(acc + lanes + c, v);
@@ -440,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
   __syncthreads();
   fence_after();
-  if (warp == 9) tmem_free(tmem, kTmemCols);
+  if (warp == 17) tmem_free(tmem, kTmemCols);
 }
 
 // gv and gk from the query heads' parts, in the order of the heads; four
