@@ -172,17 +172,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ksteps = (a.D + 15) / 16;
     Ring<kStages> ts, ta;       // slots of the scores' and of the accumulating products
     unsigned n = 0;             // subtiles whose scores were issued
+    // low words of the descriptors, in units of 16 bytes
+    constexpr uint32_t kP = kPanel >> 4, kSP = kSubPanel >> 4;
+    const uint32_t hi = (uint32_t)(smem_desc(0, 16, 1024) >> 32), hi_mn = (uint32_t)(smem_desc(0, kSubPanel, 1024) >> 32);
+    const uint32_t r1_lo = (uint32_t)smem_desc(smem_addr(r1), 16, 1024), r2_lo = (uint32_t)smem_desc(smem_addr(r2), 16, 1024),
+                   t_lo = (uint32_t)smem_desc(smem_addr(st), 16, 1024), tm_lo = (uint32_t)smem_desc(smem_addr(st), kSubPanel, 1024),
+                   sub = sub_bytes >> 4;
     auto scores = [&]() {
       const int s = n & 1;
-      const uint32_t t = smem_addr(st + ts.slot * 2 * sub_bytes);
-      for (int k = 0; k < ksteps; ++k) {
-        const uint32_t ro = (k / 4) * kPanel + (k % 4) * 32, to = (k / 4) * kSubPanel + (k % 4) * 32;
-        mma_ss(s_at(s), smem_desc(smem_addr(r1) + ro, 16, 1024), smem_desc(t + to, 16, 1024), f.idesc_s, k > 0);
-      }
-      for (int k = 0; k < ksteps; ++k) {
-        const uint32_t ro = (k / 4) * kPanel + (k % 4) * 32, to = (k / 4) * kSubPanel + (k % 4) * 32;
-        mma_ss(dp_at(s), smem_desc(smem_addr(r2) + ro, 16, 1024), smem_desc(t + sub_bytes + to, 16, 1024), f.idesc_dp, k > 0);
-      }
+      const uint32_t t1 = t_lo + ts.slot * 2 * sub, t2 = t1 + sub, sd = s_at(s), dd = dp_at(s);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < ksteps)
+          mma_ss(sd, r1_lo + k / 4 * kP + k % 4 * 2, hi, t1 + k / 4 * kSP + k % 4 * 2, hi, f.idesc_s, k > 0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < ksteps)
+          mma_ss(dd, r2_lo + k / 4 * kP + k % 4 * 2, hi, t2 + k / 4 * kSP + k % 4 * 2, hi, f.idesc_dp, k > 0);
       mma_commit(sfull + 8 * s);
       ts.next();
       ++n;
@@ -206,11 +212,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = m & 1;
       if (!(ok = bar_wait(ready + 8 * ta.slot, ta.phase, guard) && bar_wait(pfull + 8 * s, (m / 2) & 1u, guard))) break;
       fence_after();
-      const uint32_t t = smem_addr(st + ta.slot * 2 * sub_bytes);
+      const uint32_t t1 = tm_lo + ta.slot * 2 * sub, t2 = t1 + sub, sd = s_at(s), dd = dp_at(s);
 #pragma unroll
       for (int k = 0; k < kSub / 16; ++k) {
-        if (KV) mma_ts(acc1, s_at(s) + k / 2 * 32 + k % 2 * 8, smem_desc(t + sub_bytes + k * 2048, kSubPanel, 1024), f.idesc_acc, m > 0 || k > 0);
-        mma_ts(acc2, dp_at(s) + k / 2 * 32 + k % 2 * 8, smem_desc(t + k * 2048, kSubPanel, 1024), f.idesc_acc, m > 0 || k > 0);
+        const uint32_t at = k / 2 * 32 + k % 2 * 8;
+        if (KV) mma_ts(acc1, sd + at, t2 + k * 128, hi_mn, f.idesc_acc, m > 0 || k > 0);
+        mma_ts(acc2, dd + at, t1 + k * 128, hi_mn, f.idesc_acc, m > 0 || k > 0);
       }
       mma_commit(done + 8 * s);
       mma_commit(tempty + 8 * ta.slot);
