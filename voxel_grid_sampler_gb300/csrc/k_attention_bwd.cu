@@ -197,9 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       fence_after();
       scores();
+      cur = next(cur);
     }
     for (unsigned m = 0; ok; ++m) {  // m: subtile whose P and dS are consumed
-      cur = next(cur);
       const bool more = cur.head < heads;
       if (more) {
         // the stage's previous P and dS must have been read
@@ -210,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         scores();
       }
       const int s = m & 1;
-      if (!(ok = bar_wait(ready + 8 * ta.slot, ta.phase, guard) && bar_wait(pfull + 8 * s, (m / 2) & 1u, guard))) break;
+      // (its writers waited for `ready`: what that covers is visible here too)
+      if (!(ok = bar_wait(pfull + 8 * s, (m / 2) & 1u, guard))) break;
       fence_after();
       const uint32_t t1 = tm_lo + ta.slot * 2 * sub, t2 = t1 + sub, sd = s_at(s), dd = dp_at(s);
 #pragma unroll
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(tempty + 8 * ta.slot);
       ta.next();
       if (!more) break;
+      cur = next(cur);
     }
     mma_commit(accfull);
     mma_commit(drain);
