@@ -42,7 +42,8 @@
  *
  *   Limits: each dimension in [2, 2^20]; D*H*W < 2^32 voxels; bins in [8, 64];
  *   LNCC window odd and >= 3; channels of a sampled volume in [1, 4]; a
- *   moving or sampled volume below 2^31 voxels.
+ *   moving or sampled volume below 2^31 voxels.  The token operators state
+ *   their own conventions and limits below.
  */
 #ifndef FFDP_H
 #define FFDP_H
@@ -453,7 +454,9 @@ size_t ffdp_static_scratch_bytes(void);
  * inputs into shared memory with asynchronous bulk copies and wait for each
  * with a time limit (1 s).  A wait that runs out marks the current device's
  * error word, the kernel finishes without touching the copies' data, and the
- * losses of that call are written as NaN (its other outputs are invalid).
+ * losses of that call are written as NaN (its other outputs are invalid).  The
+ * token operators bound the waits of their kernels in the same way and mark the
+ * same word; all outputs of such a call are invalid.
  * This call synchronises the current device (the one exception to "no call
  * blocks on the device"), stores 1 in *flag if the word was marked since the
  * last call and 0 otherwise, and clears the word. */

@@ -167,17 +167,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t a, float* r) {
       : "r"(a));
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* u) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(a),
-      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-      : "memory");
-}
-// Fragments: 16 lanes of TMEM by 8 N columns.  Thread i holds of lane i / 4 the
-// columns 8 g + 2 (i mod 4) and + 1 in registers 4 g and 4 g + 1, and of lane
-// i / 4 + 8 the same columns in the next two.
 __device__ __forceinline__ void tmem_ld_frag16(uint32_t a, float* r) {  // 128 columns
   uint32_t* u = reinterpret_cast<uint32_t*>(r);
   asm volatile(
@@ -248,19 +237,9 @@ __host__ __device__ constexpr uint32_t mma_idesc(bool bf16, bool a_mn, bool b_mn
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A B, both operands in shared memory; one thread issues.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n"
-      "  .reg .pred p;\n"
-      "  setp.ne.b32 p, %4, 0;\n"
-      "  tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
-      "}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-// The same with descriptors as two words: only the start address, in the low
-// word, changes from one instruction of a product to the next.
+// D[tmem] (+)= A B, both operands in shared memory; one thread issues.  The
+// descriptors come as two words: only the start address, in the low word, changes
+// from one instruction of a product to the next.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
                                        bool add) {
   asm volatile(
@@ -275,6 +254,7 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi,
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
+// A in TMEM (two 16-bit elements per column, K along the columns).
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
   asm volatile(
       "{\n"
@@ -285,17 +265,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
       "  tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
       "}\n" ::"r"(d),
       "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-// A in TMEM (two 16-bit elements per column, K along the columns).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n"
-      "  .reg .pred p;\n"
-      "  setp.ne.b32 p, %4, 0;\n"
-      "  tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-      "}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
 }
 // Arrives on `bar` when this thread's matrix instructions so far are done.
