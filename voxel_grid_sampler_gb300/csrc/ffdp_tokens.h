@@ -79,7 +79,7 @@ struct FewArgs {
   float c, cap_in, cap2;  // scale log2 e; 2 log2 e scale / cap, cap log2 e
   float* part;            // as the forward kernel's
 };
-int few_splits(int64_t pairs, int64_t keys, int sms);
+int few_splits(int64_t pairs, int64_t keys, int rows, int sms);
 cudaError_t launch_attention_few(int dt, const AttnArgs& a, const FewArgs& f, cudaStream_t s);
 size_t attention_bwd_bytes(const AttnArgs& a, int sms);
 cudaError_t launch_attention_bwd(int dt, const AttnArgs& a, int sms, void* ws, cudaStream_t s);

@@ -946,7 +946,7 @@ AttnPlan attention_plan(const AttnArgs& a, int sms) {
   const int64_t least = (p.nk + kMaxCodes - 1) / kMaxCodes;
   if (s < least) s = least;
   p.splits = (int)(s < 1 ? 1 : s);
-  if (p.few) p.splits = few_splits((int64_t)a.B * a.Hk, a.Sk, sms);
+  if (p.few) p.splits = few_splits((int64_t)a.B * a.Hk, a.Sk, a.G * a.Sq, sms);
   const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
   p.ranges_bytes = round256((size_t)a.B * p.nq * sizeof(DocRange)) + round256((size_t)a.B * p.nk * sizeof(DocRange));
   p.part_bytes = p.splits > 1 ? round256((size_t)rows * p.splits * (a.D + 1) * 4) : 0;
