@@ -36,6 +36,15 @@ __device__ __forceinline__ void mma16816<__nv_bfloat16>(float* c, const uint32_t
 
 __device__ __forceinline__ uint4 load16(const void* p) { return __ldg(static_cast<const uint4*>(p)); }
 
+template <class T>
+struct IsHalf {
+  static constexpr bool value = false;
+};
+template <>
+struct IsHalf<__half> {
+  static constexpr bool value = true;
+};
+
 // An 8 x 8 matrix of 16-bit elements, transposed across the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t d;
@@ -228,7 +237,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attn_few(const At
             for (int j = 0; j < 4; ++j) o[t][c][j][y] *= w, o[t][c][j][2 + y] *= w;
         }
     }
-    uint32_t p[NT][2];  // P^T as B operands: keys 0-7 and 8-15
+    // P^T as B operands: keys 0-7 and 8-15.  bfloat16 keeps 8 bits of a weight,
+    // and one query's few large weights do not average that away: what the
+    // rounding leaves goes through a second product.
+    constexpr bool kRest = !IsHalf<T>::value;
+    uint32_t p[NT][2], rest[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const float m0 = m[t][0] == -INFINITY ? 0.0f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.0f : m[t][1];
@@ -237,7 +250,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attn_few(const At
         const float p0 = ex2(s[t][2 * e] - m0), p1 = ex2(s[t][2 * e + 1] - m1);
         l[t][0] += p0;
         l[t][1] += p1;
-        p[t][e] = transpose8(pack2<T>(p0, p1));
+        const uint32_t w = pack2<T>(p0, p1);
+        p[t][e] = transpose8(w);
+        if (kRest) rest[t][e] = transpose8(pack2<T>(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xffff0000u)));
       }
     }
 #pragma unroll
@@ -251,7 +266,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attn_few(const At
         const uint32_t v[4] = {__byte_perm(w[0][j], w[1][j], 0x5410), __byte_perm(w[0][j], w[1][j], 0x7632),
                                __byte_perm(w[2][j], w[3][j], 0x5410), __byte_perm(w[2][j], w[3][j], 0x7632)};
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma16816<T>(o[t][c][j], v, p[t][0], p[t][1]);
+        for (int t = 0; t < NT; ++t) {
+          mma16816<T>(o[t][c][j], v, p[t][0], p[t][1]);
+          if (kRest) mma16816<T>(o[t][c][j], v, rest[t][0], rest[t][1]);
+        }
       }
     }
   }
