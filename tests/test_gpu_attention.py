@@ -279,3 +279,47 @@ def test_few_rows_in_every_packing(ffdp, G, Sq):
     # 16 rows per key head, just above, tiles of several heads that fill 128 rows or do not
     t, more = _inputs(24, 2, Sq, 333, 2 * G, 2, 72, BF16, axes=3, docs=2)
     _check(ffdp, t, more, train=G < 16, causal=True, cap=10.0)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("kind", ["all", "bias", "causal", "documents", "one", "nan"])
+@pytest.mark.parametrize("Sq,D", [(100, 64), (300, 32), (257, 40)])
+def test_odd_number_of_query_tiles(ffdp, Sq, D, kind, dtype):
+    # enough heads that the keys are not split over CTAs; the last tile of each
+    # head has a CTA to itself
+    bias, docs = kind == "bias", {"documents": 6, "one": 1, "nan": 2}.get(kind, 0)
+    t, more = _inputs(Sq, 2, Sq, 530, 80, 80, D, dtype, axes=3 if bias else 0, docs=docs)
+    if kind == "one":  # a single visible key in a single tile, and sequences without any
+        more["doc_q"] = torch.zeros_like(more["doc_q"])
+        more["doc_k"] = torch.full_like(more["doc_k"], -1)
+        more["doc_k"][0, 400] = 0
+    if kind != "nan":
+        _check(ffdp, t, more, causal=kind == "causal", train=False)
+        return
+    # garbage in the keys that no row sees
+    more["doc_q"] = torch.zeros_like(more["doc_q"])
+    hidden = (more["doc_k"] != 0)[:, :, None, None]
+    o, lse = _check(ffdp, t, more, train=False)
+    p = ffdp.attention_params(float(torch.tensor(D ** -0.5, dtype=torch.float32)))
+    o2, lse2 = ffdp.ffdp_attention_fwd(t["q"], t["k"].masked_fill(hidden, float("nan")),
+                                       t["v"].masked_fill(hidden, float("inf")), p, **more)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("Sq,Sk,docs,causal,cap", [(100, 100, 7, True, 0.0), (30, 30, 0, False, 0.0), (31, 40, 0, True, 3.0),
+                                                   (300, 300, 40, False, 0.0)])
+def test_gradients_of_rows_with_few_keys(ffdp, Sq, Sk, docs, causal, cap, dtype):
+    # two roundings of one size (dS, the result) are sqrt(2) of one; the rounding
+    # of o must not add a third: that is 1.6 and more on these inputs
+    t, more = _inputs(Sq, 3, Sq, Sk, 4, 2, 64, dtype, axes=2 if docs == 7 else 0, docs=docs)
+    if docs:
+        more["doc_k"] = more["doc_q"] = (torch.arange(Sq, device="cuda") * docs // Sq).int().expand(3, Sq).contiguous()
+    q, k, v, go = t["q"], t["k"], t["v"], t["go"]
+    o, lse, gq, gk, gv = _check(ffdp, t, more, cap=cap, causal=causal)
+    scale = float(torch.tensor(64 ** -0.5, dtype=torch.float32))
+    want = ref.attention(q, k, v, scale, cap, go=go, causal=causal, **more)
+    for n, x in (("gq", gq), ("gk", gk)):
+        w = want[n][0].double().cpu()
+        off, own = ((y.double() - w).norm() for y in (x.cpu(), w.to(dtype)))
+        assert off <= 1.55 * own, (n, float(off / own))

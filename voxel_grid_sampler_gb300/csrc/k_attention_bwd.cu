@@ -15,6 +15,12 @@
 // accumulating products.  Warps: 0-7 and 8-15 even and odd subtiles, 16 loads
 // (TMA), 17 multiplies, 18 and 19 prepare each subtile's lse, delta, positions,
 // documents and non-finite rows.
+//
+// 2 x 4096 queries and keys, 16 / 4 heads of 128 in bfloat16: 539 us for the keys'
+// pass and 449 us for the queries', 974 TFLOP/s counting the seven products; in
+// five documents with capped scores 320 and 254 us.  The tensor cores are active
+// half of the time: a subtile's products wait for its weights, the weights for the
+// products, and the one issuing thread takes about 1000 cycles per subtile.
 #include <atomic>
 
 #include "ffdp_attention.cuh"
@@ -478,6 +484,102 @@ __global__ void __launch_bounds__(256) k_attn_heads(const BwdArgs f) {
   *reinterpret_cast<uint2*>(o) = make_uint2(pack2<T>(t.x, t.y), pack2<T>(t.z, t.w));
 }
 
+// dP - delta cancels in rows that see few keys (all of it with one key), and the
+// rounding of o to 16 bits then shows in the gradients: with 100 tokens in seven
+// causal documents gq and gk were 1.8 times as inexact as their own rounding makes
+// them, and are 1.4 times.  Rows that see fewer than 32 keys take delta = sum_j P_j
+// dP_j from the keys instead, one key per lane, after k_attn_delta (inside it the
+// registers cost all rows more than they gave: 33 us instead of 12 + 6).
+constexpr int kFewKeys = 32;
+
+// The keys that row (b, i) sees, if they are fewer than kFewKeys and easily
+// found (documents: in at most two key tiles): their number, else 0.
+__device__ __forceinline__ int few_keys(const AttnArgs& a, const DocRange* dk, int b, int i, int* list, int lane) {
+  const int limit = key_limit(a, prefix_of(a, b), i);
+  if (!a.doc_q) {
+    if (limit >= kFewKeys) return 0;
+    list[lane] = lane;
+    return limit;
+  }
+  const int doc = a.doc_q[b * a.doc_q_sb + i];
+  // most rows of long documents are told by the keys beside them, in one round of loads
+  const int before = i + a.Sk - a.Sq - 31 + lane, after = before + 31;
+  const bool in0 = before >= 0 && before < limit && a.doc_k[b * a.doc_k_sb + before] == doc;
+  const bool in1 = after >= 0 && after < limit && a.doc_k[b * a.doc_k_sb + after] == doc;
+  if (doc < 0 || __all_sync(0xffffffffu, in0) || __all_sync(0xffffffffu, in1)) return 0;
+  const int tiles = (limit + kTile - 1) / kTile;
+  const DocRange* ranges = dk + (int64_t)b * ((a.Sk + kTile - 1) / kTile);
+  int n = 0, seen = 0;
+  for (int t0 = 0; t0 < tiles; t0 += 32) {
+    bool in = false;
+    if (t0 + lane < tiles) {
+      const DocRange r = ranges[t0 + lane];
+      in = r.lo <= doc && doc <= r.hi;
+    }
+    unsigned mask = __ballot_sync(0xffffffffu, in);
+    if ((seen += __popc(mask)) > 2) return 0;
+    for (; mask; mask &= mask - 1)
+      for (int c = 0; c < kTile; c += 32) {
+        const int j = (t0 + __ffs(mask) - 1) * kTile + c + lane;
+        const bool see = j < limit && a.doc_k[b * a.doc_k_sb + j] == doc;
+        const unsigned hit = __ballot_sync(0xffffffffu, see);
+        if (n + __popc(hit) >= kFewKeys) return 0;
+        if (see) list[n + __popc(hit & ((1u << lane) - 1u))] = j;
+        n += __popc(hit);
+      }
+  }
+  return n;
+}
+
+// A warp per token and kFewHeads of its heads.
+constexpr int kFewHeads = 4;
+template <class T>
+__global__ void __launch_bounds__(256) k_attn_delta_few(const AttnArgs a, const DocRange* dk, int tokens) {
+  __shared__ int lists[8][kFewKeys];
+  const int lane = threadIdx.x % 32, groups = (a.Hq + kFewHeads - 1) / kFewHeads;
+  int* list = lists[threadIdx.x / 32];
+  const int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  if (w >= (int64_t)a.B * tokens * groups) return;
+  const int h0 = (int)(w % groups) * kFewHeads, i = (int)(w / groups % tokens), b = (int)(w / groups / tokens);
+  const int n = few_keys(a, dk, b, i, list, lane);
+  if (n == 0) return;
+  __syncwarp();
+  for (int h = h0; h < min(h0 + kFewHeads, a.Hq); ++h) {
+    float* delta = a.delta + ((int64_t)b * a.Hq + h) * a.Sq + i;
+    if (!(fabsf(*delta) < INFINITY)) continue;  // a row with a NaN stays one
+    float part = 0.0f;
+    if (lane < n) {
+      const int j = list[lane], g = h / a.G;
+      const T* qp = static_cast<const T*>(a.q.p) + b * a.q.sb + (int64_t)i * a.q.st + h * a.q.sh;
+      const T* op = static_cast<const T*>(a.go.p) + b * a.go.sb + (int64_t)i * a.go.st + h * a.go.sh;
+      const T* kp = static_cast<const T*>(a.k.p) + b * a.k.sb + (int64_t)j * a.k.st + g * a.k.sh;
+      const T* vp = static_cast<const T*>(a.v.p) + b * a.v.sb + (int64_t)j * a.v.st + g * a.v.sh;
+      float s = 0.0f, dp = 0.0f;
+#pragma unroll 2
+      for (int d = 0; d < a.D; d += 8) {
+        const uint4 q4 = *reinterpret_cast<const uint4*>(qp + d), o4 = *reinterpret_cast<const uint4*>(op + d);
+        const uint4 k4 = *reinterpret_cast<const uint4*>(kp + d), v4 = *reinterpret_cast<const uint4*>(vp + d);
+        const T *qe = reinterpret_cast<const T*>(&q4), *oe = reinterpret_cast<const T*>(&o4);
+        const T *ke = reinterpret_cast<const T*>(&k4), *ve = reinterpret_cast<const T*>(&v4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s = fmaf(to_f32<T>(qe[e]), to_f32<T>(ke[e]), s);
+          dp = fmaf(to_f32<T>(oe[e]), to_f32<T>(ve[e]), dp);
+        }
+      }
+      s *= a.scale;
+      if (a.cap > 0.0f) s = a.cap * tanhf(s / a.cap);
+      for (int x = 0; x < a.axes; ++x)
+        s -= a.slopes[h * a.axes + x] * fabsf(a.pos_q[b * a.pos_q_sb + (int64_t)i * a.axes + x] -
+                                               a.pos_k[b * a.pos_k_sb + (int64_t)j * a.axes + x]);
+      part = ex2((s - a.lse[((int64_t)b * a.Hq + h) * a.Sq + i]) * kLog2e) * dp;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == 0) *delta = part;
+  }
+}
+
 // delta = sum_d go o, 16 lanes per row.
 template <class T>
 __global__ void __launch_bounds__(256) k_attn_delta(const AttnArgs a) {
@@ -537,7 +639,7 @@ namespace {
 // fewer than four CTAs per SM, one query head each, their parts summed after: the
 // parts' traffic (8 bytes per element, twice) costs less than the last wave's
 // idle SMs and the longest document's lone CTA (2 x 4096 tokens in five
-// documents, 16 / 4 heads of 128: 438 us by key head).
+// documents, 16 / 4 heads of 128: 438 us by key head, 320 + 35 us apart).
 bool heads_apart(const AttnArgs& a, int sms) {
   return a.G > 1 && (int64_t)a.B * a.Hk * ((a.Sk + kTile - 1) / kTile) < 4 * (int64_t)sms;
 }
@@ -587,6 +689,15 @@ cudaError_t launch_attention_bwd(int dt, const AttnArgs& args, int sms, void* ws
     note_launch_begin("k_attn_delta", s);
     FFDP_TOK_SWITCH16(dt, T, (k_attn_delta<T><<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(a)));
     note_launch_end(s);
+    // tokens that may see few keys: with documents any, else those before the causal line's 32nd key
+    int64_t tokens = a.doc_q || a.Sk < kFewKeys ? a.Sq : (a.causal ? (int64_t)kFewKeys - 1 - (a.Sk - a.Sq) : 0);
+    if (tokens > a.Sq) tokens = a.Sq;
+    if (tokens > 0) {
+      const int64_t warps = a.B * tokens * ((a.Hq + kFewHeads - 1) / kFewHeads);
+      note_launch_begin("k_attn_delta_few", s);
+      FFDP_TOK_SWITCH16(dt, T, (k_attn_delta_few<T><<<(unsigned)((warps + 7) / 8), 256, 0, s>>>(a, f.dk, (int)tokens)));
+      note_launch_end(s);
+    }
   }
   // an empty side loads nothing: any valid address serves its maps
   HeadsView q = a.q, k = a.k, v = a.v, go = a.go;

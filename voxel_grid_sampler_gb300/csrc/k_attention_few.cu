@@ -11,6 +11,11 @@
 // instructions' work is padding and their rate was the bound.  Both products are
 // free to permute an index (the summed channels of k, the output channels of
 // v), so that the 16 bytes a thread loads are its own operands.
+//
+// One query over 13440 keys, batch 4, 16 / 4 heads of 128 in bfloat16 (110 MB): 32 us,
+// 3.5 TB/s, and 5 us for the join; without the distance bias 26 us.  What is left
+// above the 16 us of the bytes is the bias (32 elements per thread and block), the
+// loads of the next block that wait for it, and the start and end of each CTA.
 #include "ffdp_attention.cuh"
 
 namespace ffdp {

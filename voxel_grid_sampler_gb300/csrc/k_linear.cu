@@ -3,6 +3,14 @@
 // C[m][n] = sum_k A(m, k) B(n, k) + epilogue: the forward product (x w^T), gx =
 // gz w and gw = gz^T x are this product with operands that are contiguous
 // along the contraction (K-major) or across it (MN-major).
+//
+// Measured in bfloat16 (the rate of a large plain library product: 1878 TFLOP/s):
+// 13440 tokens of 4096 to 4096 channels 253 us, 1780 TFLOP/s; of 4096 to 1024 and
+// its two gradients 76 us each, 1480 TFLOP/s (53 x 4 tiles of 256 x 256 on 76 pairs
+// of CTAs: the third wave is 79 % full); of 1024 to 4096 with bias and GELU 102 us,
+// 1105 TFLOP/s (83 us without the activation: the epilogue's arithmetic, not the
+// tensor cores, which are active 56 % of the time); one token of 1024 to 4096 with
+// split sums 13 + 9 us, launches included.
 #include <atomic>
 
 #include "ffdp_tc.cuh"

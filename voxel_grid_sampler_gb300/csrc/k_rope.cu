@@ -3,7 +3,10 @@
 // Pair k of a head turns by t = pos[token][axis(k)] * freq[k]; the angle is the
 // same for every head of every tensor of a token, so a CTA computes the sines
 // and cosines of its tokens once into shared memory and then streams the heads.
-// Bound by HBM: each element is read and written once.
+// Bound by HBM: each element is read and written once, in accesses of 16 bytes
+// wherever widths, strides and addresses allow.  2 x 13440 tokens, q and k of 16
+// heads of 64 in bfloat16 (220 MB): 40 us, 5.5 TB/s, 81 % of a plain copy's rate;
+// one token: 3 us, a launch.
 #include "ffdp_tokens.h"
 
 namespace ffdp {
