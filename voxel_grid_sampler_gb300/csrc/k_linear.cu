@@ -497,7 +497,10 @@ __global__ void __launch_bounds__(kGzWarps * 32) k_linear_gz(const LinearGradArg
   float t = 0.0f;
 #pragma unroll
   for (int w = 0; w < kGzWarps; ++w) t += sums[w][c];
-  a.partial[(int64_t)blockIdx.y * a.N + col] = t;
+  if (gridDim.y == 1)
+    static_cast<T*>(a.gb)[col] = from_f32<T>(t);
+  else
+    a.partial[(int64_t)blockIdx.y * a.N + col] = t;
 }
 
 // Sums of the chunks, 32 columns per CTA, 8 threads per column.
@@ -566,7 +569,10 @@ int div_up(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 // Pairs of CTAs on tiles of 256 x 256 where those fill three quarters of the
 // pairs.  Else the tile is 128 x 256 where that gives every SM a tile (the least operand
 // traffic per product), else 128 x 128 or 128 x 64; a product with still fewer
-// tiles than SMs splits its contraction, at least 4 blocks of 64 per split.
+// tiles than SMs splits its contraction: at least 16 blocks of 64 per split, and
+// only where that takes 32 blocks off the longest, since the join is a launch of
+// its own (one token, 1024 to 4096 channels: 9.9 us whole, 11.8 in two; 64 tokens,
+// 1024 to 1024: 7.8 whole, 10.9 in four; 16 tokens, 4096 to 256: 16.5 whole, 12.6 in four).
 LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int sms) {
   LinearPlan l{};
   const int64_t tm = (M + kBM - 1) / kBM;
@@ -581,8 +587,9 @@ LinearPlan linear_plan(int64_t M, int64_t N, int64_t K, int sms) {
   const int64_t tiles = tm * ((N + l.bn - 1) / l.bn), kb = (K + kBK - 1) / kBK;
   int64_t s = 1;
   if (tiles * 2 <= sms) s = sms / tiles;
-  if (s > kb / 4) s = kb / 4;
-  l.splits = (int)(s < 1 ? 1 : s);
+  if (s > kb / 16) s = kb / 16;
+  if (s < 1 || kb - (kb + s - 1) / s < 32) s = 1;
+  l.splits = (int)s;
   l.partial_bytes = l.splits > 1 ? (size_t)tiles * l.splits * l.bn * kBM * 4 : 0;
   return l;
 }
@@ -630,8 +637,11 @@ cudaError_t launch_linear(int dt, const LinearArgs& a, int sms, float* partial, 
   });
 }
 
-// Chunks of rows: four CTAs per SM, at least 16 rows each (two per warp).
+// Chunks of rows: four CTAs per SM, at least 16 rows each (two per warp).  Up to
+// 128 rows are one chunk, whose sums need no second kernel (3 us, and 3 us of the
+// call).
 int linear_grad_chunks(int M, int N, int sms) {
+  if (M <= 128) return 1;
   const int cols = div_up(N, kGzCols);
   int c = div_up(4 * (int64_t)sms, cols);
   const int most = div_up(M, 2 * kGzWarps);
@@ -644,7 +654,7 @@ cudaError_t launch_linear_grad(int dt, const LinearGradArgs& a, cudaStream_t s) 
   note_launch_begin("k_linear_gz", s);
   FFDP_TOK_SWITCH16(dt, T, (k_linear_gz<T><<<dim3(div_up(a.N, kGzCols), a.chunks), kGzWarps * 32, 0, s>>>(a, rows)));
   note_launch_end(s);
-  if (a.gb) {
+  if (a.gb && a.chunks > 1) {
     note_launch_begin("k_linear_gb", s);
     FFDP_TOK_SWITCH16(dt, T, (k_linear_gb<T><<<div_up(a.N, 32), 256, 0, s>>>(a)));
     note_launch_end(s);
