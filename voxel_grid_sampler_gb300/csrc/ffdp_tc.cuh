@@ -79,6 +79,19 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, unsigned parity, const Gu
 __device__ __forceinline__ bool bar_wait_warp(uint32_t bar, unsigned parity, const Guard& g) {
   return __all_sync(0xffffffffu, bar_wait(bar, parity, g));
 }
+// Two kernels of a stream that do not need each other's results: the first says at
+// its start that the second, launched with `overlapping`, may start once all of its
+// CTAs have; the second's CTAs take the SMs that the first's last CTAs leave idle,
+// and end only after the first has, so that what follows it follows both.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+inline cudaLaunchAttribute overlapping() {
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
 // For a drain after the loops: the limit holds, the dead flag does not end it.
 __device__ __forceinline__ void bar_drain(uint32_t bar, unsigned parity) {
   const unsigned long long t0 = now_ns();
