@@ -323,3 +323,24 @@ def test_gradients_of_rows_with_few_keys(ffdp, Sq, Sk, docs, causal, cap, dtype)
         w = want[n][0].double().cpu()
         off, own = ((y.double() - w).norm() for y in (x.cpu(), w.to(dtype)))
         assert off <= 1.55 * own, (n, float(off / own))
+
+
+@pytest.mark.parametrize("B", [3, 600])
+@pytest.mark.parametrize("causal", [False, True])
+def test_documents_of_few_and_many_sequences(ffdp, B, causal):
+    # work is ordered by length up to 1024 units, taken as it comes above
+    t, more = _inputs(B, B, 150, 150, 2, 1, 16, F16, docs=5)
+    _check(ffdp, t, more, causal=causal)
+
+
+@pytest.mark.parametrize("axes", [0, 3])
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_query_tiles_of_a_pair_that_see_different_keys(ffdp, D, axes):
+    # the pair's first query tile lies in a short document, the second reaches
+    # into a long one: the first skips many key tiles in the middle of the walk
+    t, more = _inputs(D, 2, 1954, 1954, 8, 8, D, BF16, axes=axes)
+    ids = torch.full((1954,), -1, dtype=torch.int32, device="cuda")
+    for i, (a, b) in enumerate(((0, 317), (317, 952), (952, 1905))):
+        ids[a:b] = i
+    more["doc_q"] = more["doc_k"] = ids.expand(2, 1954).contiguous()
+    _check(ffdp, t, more)

@@ -44,6 +44,7 @@ constexpr unsigned kTmemCols = 512;
 struct BwdArgs {
   AttnArgs a;
   const DocRange *dq, *dk;
+  const int *by_keys, *by_queries;  // documents: sequences' tiles, longest walks first, or NULL
   int panels;
   uint32_t idesc_s, idesc_dp, idesc_acc;
   float c;             // |scale| log2 e
@@ -83,7 +84,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool by_head = KV && f.part;  // a query head per CTA, not a key head
   const int H = KV && !by_head ? a.Hk : a.Hq, tiles = ((KV ? a.Sk : a.Sq) + kTile - 1) / kTile;
   int tile, bh;
-  if (a.causal) {
+  const int* order = KV ? f.by_keys : f.by_queries;
+  if (order) {
+    const int at = blockIdx.x / H, unit = order[at], seq = unit / tiles;
+    tile = unit - seq * tiles;
+    bh = seq * H + blockIdx.x - at * H;
+  } else if (a.causal) {
     tile = blockIdx.x / (a.B * H);
     bh = blockIdx.x - tile * (a.B * H);
     if (!KV) tile = tiles - 1 - tile;
@@ -664,7 +670,8 @@ size_t part_bytes(const AttnArgs& a, int sms) {
 
 size_t attention_bwd_bytes(const AttnArgs& a, int sms) {
   return round256((size_t)a.B * a.Hq * a.Sq * 4) + round256((size_t)a.B * ((a.Sq + kTile - 1) / kTile) * sizeof(DocRange)) +
-         round256((size_t)a.B * ((a.Sk + kTile - 1) / kTile) * sizeof(DocRange)) + part_bytes(a, sms);
+         round256((size_t)a.B * ((a.Sk + kTile - 1) / kTile) * sizeof(DocRange)) + part_bytes(a, sms) +
+         round256((size_t)order_units(a, kByKeys) * 4) + round256((size_t)order_units(a, kByQueries) * 4);
 }
 
 cudaError_t launch_attention_bwd(int dt, const AttnArgs& args, int sms, void* ws, cudaStream_t s) {
@@ -684,6 +691,12 @@ cudaError_t launch_attention_bwd(int dt, const AttnArgs& args, int sms, void* ws
     e = launch_doc_ranges(a, dq, dk, s);
     f.dq = dq;
     f.dk = dk;
+    const int nk = order_units(a, kByKeys), nq = order_units(a, kByQueries);
+    int* keys = reinterpret_cast<int*>(w + part_bytes(a, sms));
+    int* queries = keys + round256((size_t)nk * 4) / 4;
+    f.by_keys = nk ? keys : nullptr;
+    f.by_queries = nq ? queries : nullptr;
+    if (e == cudaSuccess && (nk || nq)) e = launch_doc_order(a, dq, dk, nullptr, nk ? keys : nullptr, nq ? queries : nullptr, s);
   }
   if (e == cudaSuccess) e = device_error_word(&f.error);
   if (e != cudaSuccess) return e;

@@ -38,12 +38,14 @@ constexpr float kRescale = 8.0f;  // O and the sum are rescaled when the maximum
 struct FwdArgs {
   AttnArgs a;
   const DocRange *dq, *dk;
+  const int* order; // documents: sequences' pairs of query tiles, longest first, or NULL
   int packed;       // rows of a tile are `rh` tokens of `gb` heads
   int rh, gb;
   int tiles, pairs; // query tiles and pairs of them per key head
   int splits, nk;   // splits of the key tiles, key tiles in all
   int items, sms;
   int whole;        // items with two tiles, where order by length does not matter
+  Divisor by_hks, by_all;  // Hk splits, pairs
   Divisor by_splits, by_pairs, by_hk, by_g, by_bgs, by_rh;  // pairs of two tiles; bgs: B Hk splits
   int panels, stages;
   uint32_t idesc_s, idesc_o;
@@ -80,7 +82,13 @@ __device__ __forceinline__ Item item_of(const FwdArgs& f, int w) {
   const AttnArgs& a = f.a;
   Item x;
   int pair, bg;
-  if (a.causal) {  // the longest rows first
+  if (!PACKED && f.order) {
+    const int at = div_by(w, f.by_hks), unit = f.order[at], rest = w - at * f.by_hks.d, b = div_by(unit, f.by_all);
+    pair = unit - b * f.by_all.d;
+    bg = div_by(rest, f.by_splits);
+    x.split = rest - bg * f.splits;
+    bg += b * a.Hk;
+  } else if (a.causal) {  // the longest rows first
     pair = div_by(w, f.by_bgs);
     w -= pair * f.by_bgs.d;
     pair = f.pairs - 1 - pair;
@@ -121,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ CUtensorMap mv, const FwdArgs f) {
   extern __shared__ char raw[];
   char* base = reinterpret_cast<char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t bars[6 + 5 * kMaxStages + 9];
+  __shared__ uint64_t bars[6 + 7 * kMaxStages + 9];
   __shared__ volatile unsigned dead;
   __shared__ unsigned tmem_slot;
   // the plan of an item: its visible key tiles in order, index | code << 11
@@ -138,9 +146,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t qfull = smem_addr(bars), qempty = qfull + 8, pready = qempty + 8, pfree = pready + 16, kfull = pfree + 16,
                  kempty = kfull + 8 * kMaxStages, vfull = kempty + 8 * kMaxStages, vempty = vfull + 8 * kMaxStages,
                  ready = vempty + 8 * kMaxStages, sfull = ready + 8 * kMaxStages, sread = sfull + 16, pfull = sread + 16,
-                 pvdone = pfull + 16, drain = pvdone + 16;
+                 pvdone = pfull + 16, drain = pvdone + 16, told = drain + 8;
   const Guard guard{&dead, f.error};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // this CTA's items: one of every round, and where the longest come first in turn
+  // from the front and the back of a round
+  const bool turns = f.order || a.causal;
+  auto nth = [&](unsigned k) { return (int)(k * gridDim.x + (turns && (k & 1u) ? gridDim.x - 1 - blockIdx.x : blockIdx.x)); };
   if (threadIdx.x == 0) {
     dead = 0;
     bar_init(qfull, 1);
@@ -155,6 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(vfull + 8 * i, 1);
       bar_init(vempty + 8 * i, 2);
       bar_init(ready + 8 * i, 1);
+      bar_init(told + 8 * i, 1);
+      bar_init(told + 8 * (kMaxStages + i), 1);
     }
     for (int t = 0; t < 2; ++t) {
       bar_init(sfull + 8 * t, 1);
@@ -185,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot = 0;
       unsigned phase = 0;
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < f.items; w += gridDim.x, ++k) {
+      for (int w = nth(0); ok && w < f.items; w = nth(++k)) {
         const Item x = item_of<PACKED>(f, w);
         const int prefix = prefix_of(a, x.b), buf = k & 1;
         if (!(ok = bar_wait_warp(pfree + 8 * buf, ((k >> 1) & 1u) ^ 1u, guard))) break;
@@ -258,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int slot;
         unsigned phase;
       };
-      Walk sc{(int)blockIdx.x, 0, 0, -1, 0, 0, 0}, pv = sc;
+      Walk sc{nth(0), 0, 0, -1, 0, 0, 0}, pv = sc;
       bool ok = true;
       unsigned scored = 0, done = 0;  // products S and P V issued
       bool started = false;           // O holds this item's sums
@@ -277,8 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               bar_arrive(pfree + 8 * (x.k & 1));
               started = false;
             }
-            x.w += gridDim.x;
-            ++x.k;
+            x.w = nth(++x.k);
             x.n = -1;
           }
           if (x.w >= f.items || x.k > last) return false;
@@ -349,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int slot = 0;
       unsigned phase = 0, k = 0;
       bool ok = true;
-      for (int w = blockIdx.x; ok && w < f.items; w += gridDim.x, ++k) {
+      for (int w = nth(0); ok && w < f.items; w = nth(++k)) {
         const Item it = item_of<PACKED>(f, w);
         float slope[2][3], origin[2][3], qlo[2][3], qhi[2][3];
         if (AXES && !PACKED) {
@@ -434,7 +447,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_async_smem();
           }
           __syncwarp();
-          if (lane == 0) bar_arrive(ready + 8 * slot);
+          if (lane == 0) {
+            // to the query tiles that see this key tile only: one that skips may be more
+            // than a round of slots ahead, where a barrier's parity tells it nothing
+            if (code & 3) bar_arrive(told + 8 * slot);
+            if (code >> 2) bar_arrive(told + 8 * (kMaxStages + slot));
+            bar_arrive(ready + 8 * slot);
+          }
           if (++slot == NS) slot = 0, phase ^= 1u;
         }
         __syncwarp();
@@ -448,9 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r0 = (warp % 4) * 32 + lane / 4;  // this thread's rows: r0 + 8 y, y < 4
     const int cb = 2 * (lane % 4);              // its keys: 8 g + cb + {0, 1}, g < 16
     int slot = 0;
-    unsigned phase = 0, k = 0, count = 0;       // items, key tiles of this query tile
+    unsigned phases = 0, k = 0, count = 0;      // parities of `told` by slot; items, key tiles of this query tile
     bool ok = true;
-    for (int w = blockIdx.x; ok && w < f.items; w += gridDim.x, ++k) {
+    for (int w = nth(0); ok && w < f.items; w = nth(++k)) {
       const Item it = item_of<PACKED>(f, w);
       const int b = it.b, i0 = t ? it.i0[1] : it.i0[0], i1 = t ? it.i1[1] : it.i1[0], head = t ? it.head[1] : it.head[0];
       const bool live = i1 > i0;
@@ -510,9 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int e = 0; e < tiles; ++e) {
         const int entry = plan[buf][e], code = (entry >> (11 + 2 * t)) & 3;
         if (code) {
-          if (AXES || code == kMasked) {
-            if (!(ok = bar_wait_warp(ready + 8 * slot, phase, guard))) break;
-          }
+          const uint32_t tell = told + 8 * (t * kMaxStages + slot);
+          const unsigned phase = (phases >> slot) & 1u;
+          const bool early = AXES || code == kMasked || !busy;  // else only the slot's order needs it
+          phases ^= 1u << slot;
+          if (early && !(ok = bar_wait_warp(tell, phase, guard))) break;
           const Aux& x = aux[slot];
           if (!(ok = bar_wait_warp(sfull + 8 * t, count & 1u, guard))) break;
           fence_after();
@@ -523,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) bar_arrive(pfull + 8 * t);
             ++count;
             first = false;
-            if (++slot == NS) slot = 0, phase ^= 1u;
+            if (++slot == NS) slot = 0;
             continue;
           }
           float s[128];  // row y, keys 8 g + cb and + 1: at(y, g) and + 1
@@ -745,12 +766,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
           fence_before();
+          if (!early && !(ok = bar_wait_warp(tell, phase, guard))) break;
           __syncwarp();
           if (lane == 0) bar_arrive(pfull + 8 * t);
           ++count;
           first = false;
         }
-        if (++slot == NS) slot = 0, phase ^= 1u;
+        if (++slot == NS) slot = 0;
       }
       __syncwarp();
       if (lane == 0) bar_arrive(pfree + 8 * buf);
@@ -878,6 +900,41 @@ __global__ void __launch_bounds__(256) k_doc_ranges(const AttnArgs a, DocRange* 
   if (lane == 0) (q ? dq + (int64_t)b * nq : dk + (int64_t)b * nk)[tile] = DocRange{lo, hi, pad, 0};
 }
 
+// One CTA per kind of unit: a warp counts the tiles that a unit walks, then each
+// unit's place is the number of longer ones.
+__global__ void __launch_bounds__(1024) k_doc_order(const AttnArgs a, const DocRange* dq, const DocRange* dk, int* o0, int* o1,
+                                                    int* o2) {
+  __shared__ int work[kMostUnits];
+  const int kind = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int* order = kind == kByPairs ? o0 : (kind == kByKeys ? o1 : o2);
+  if (!order) return;
+  const int nq = (a.Sq + kTile - 1) / kTile, nk = (a.Sk + kTile - 1) / kTile, tiles = nq * a.G;
+  const int per = kind == kByPairs ? (tiles + 1) / 2 : (kind == kByKeys ? nk : nq), units = a.B * per;
+  for (int u = warp; u < units; u += 32) {
+    const int b = u / per, x = u - b * per, prefix = prefix_of(a, b), other = kind == kByKeys ? nq : nk;
+    int n = 0;
+    for (int y = lane; y < other; y += 32) {
+      auto seen = [&](int q, int k) {
+        return pair_code(a, prefix, b, q * kTile, min(a.Sq, (q + 1) * kTile), k * kTile, (k + 1) * kTile, dq, dk) != kSkip;
+      };
+      if (kind == kByPairs) {
+        const int q0 = 2 * x / a.G, q1 = 2 * x + 1 < tiles ? (2 * x + 1) / a.G : q0;
+        n += seen(q0, y) || (q1 != q0 && seen(q1, y));
+      } else {
+        n += kind == kByKeys ? seen(y, x) : seen(x, y);
+      }
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) work[u] = n;
+  }
+  __syncthreads();
+  for (int u = threadIdx.x; u < units; u += 1024) {
+    int at = 0;
+    for (int v = 0; v < units; ++v) at += work[v] > work[u] || (work[v] == work[u] && v < u);
+    order[at] = u;
+  }
+}
+
 template <class T, int AXES, bool CAP, bool PACKED>
 cudaError_t run(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const FwdArgs& f, cudaStream_t s) {
   static std::atomic<unsigned long long> granted{0};
@@ -931,6 +988,14 @@ cudaError_t launch_doc_ranges(const AttnArgs& a, DocRange* dq, DocRange* dk, cud
   return cudaGetLastError();
 }
 
+cudaError_t launch_doc_order(const AttnArgs& a, const DocRange* dq, const DocRange* dk, int* pairs, int* keys, int* queries,
+                             cudaStream_t s) {
+  note_launch_begin("k_doc_order", s);
+  k_doc_order<<<pairs ? 1 : 3, 1024, 0, s>>>(a, dq, dk, pairs, keys, queries);
+  note_launch_end(s);
+  return cudaGetLastError();
+}
+
 // Rows of a query tile, and how the key tiles are split: a call whose tiles
 // leave SMs idle splits its keys over them, at least two key tiles each.
 AttnPlan attention_plan(const AttnArgs& a, int sms) {
@@ -957,7 +1022,8 @@ AttnPlan attention_plan(const AttnArgs& a, int sms) {
   p.splits = (int)(s < 1 ? 1 : s);
   if (p.few) p.splits = few_splits((int64_t)a.B * a.Hk, a.Sk, a.G * a.Sq, sms);
   const int64_t rows = (int64_t)a.B * a.Hq * a.Sq;
-  p.ranges_bytes = round256((size_t)a.B * p.nq * sizeof(DocRange)) + round256((size_t)a.B * p.nk * sizeof(DocRange));
+  p.ranges_bytes = round256((size_t)a.B * p.nq * sizeof(DocRange)) + round256((size_t)a.B * p.nk * sizeof(DocRange)) +
+                   round256((size_t)order_units(a, kByPairs) * sizeof(int));
   p.part_bytes = p.splits > 1 ? round256((size_t)rows * p.splits * (a.D + 1) * 4) : 0;
   return p;
 }
@@ -986,7 +1052,12 @@ cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, int sms, void* ws, c
   if (a.doc_q && !p.few) {
     f.dq = dq;
     f.dk = dk;
-    const cudaError_t e = launch_doc_ranges(a, dq, dk, s);
+    cudaError_t e = launch_doc_ranges(a, dq, dk, s);
+    if (e == cudaSuccess && !p.packed && order_units(a, kByPairs)) {
+      int* order = reinterpret_cast<int*>(dk) + round256((size_t)a.B * p.nk * sizeof(DocRange)) / sizeof(int);
+      e = launch_doc_order(a, dq, dk, order, nullptr, nullptr, s);
+      f.order = order;
+    }
     if (e != cudaSuccess) return e;
   }
   f.packed = p.packed;
@@ -997,6 +1068,8 @@ cudaError_t launch_attention_fwd(int dt, const AttnArgs& a, int sms, void* ws, c
   f.splits = p.splits;
   f.items = a.B * a.Hk * p.pairs * p.splits;
   f.sms = sms;
+  f.by_hks = divisor(a.Hk * p.splits);
+  f.by_all = divisor(p.pairs > 0 ? p.pairs : 1);
   f.by_splits = divisor(p.splits);
   f.whole = a.B * a.Hk * (p.tiles / 2) * p.splits;
   f.by_pairs = divisor(p.tiles / 2 > 0 ? p.tiles / 2 : 1);
