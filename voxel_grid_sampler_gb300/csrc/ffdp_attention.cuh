@@ -193,7 +193,7 @@ cudaError_t launch_doc_ranges(const AttnArgs& a, DocRange* dq, DocRange* dk, cud
 
 // Orders of work, longest first, for calls with documents: documents of unequal
 // length otherwise leave most SMs waiting for a few (2 x 4096 tokens in documents of
-// 266 to 1331, 16 / 4 heads of 128: forward 258 us in raster order, 206 us sorted and
+// 266 to 1331, 16 / 4 heads of 128: forward 258 us in raster order, 199 us sorted and
 // dealt to the CTAs from both ends, backward 573 and 512 us; the sort takes 4 us).
 // A unit is a sequence and a pair of query tiles (forward), a tile of keys or a
 // tile of queries (backward).  Above kMostUnits there are enough of each kind.

@@ -21,7 +21,7 @@
 //
 // 2 x 4096 queries and keys, 16 / 4 heads of 128 in bfloat16: 539 us for the keys'
 // pass and 449 us for the queries', 974 TFLOP/s counting the seven products; in
-// five documents with capped scores 320 and 254 us.  The tensor cores are active
+// five documents with capped scores 288 and 222 us.  The tensor cores are active
 // half of the time: a subtile's products wait for its weights, the weights for the
 // products, and the one issuing thread takes about 1000 cycles per subtile.
 #include <atomic>
@@ -658,7 +658,7 @@ namespace {
 // fewer than four CTAs per SM, one query head each, their parts summed after: the
 // parts' traffic (8 bytes per element, twice) costs less than the last wave's
 // idle SMs and the longest document's lone CTA (2 x 4096 tokens in five
-// documents, 16 / 4 heads of 128: 438 us by key head, 320 + 35 us apart).
+// documents, 16 / 4 heads of 128: 438 us by key head, 288 + 30 us apart).
 bool heads_apart(const AttnArgs& a, int sms) {
   return a.G > 1 && (int64_t)a.B * a.Hk * ((a.Sk + kTile - 1) / kTile) < 4 * (int64_t)sms;
 }

@@ -15,10 +15,10 @@
 // 384 threads start with 168 registers each, the softmax warps take 208 and
 // leave 88.
 //
-// 13440 queries and keys, 16 heads of 64 in bfloat16 with the distance bias 1752 us,
-// 422 TFLOP/s; 4096 by 4096 of them 190 us with it and 115 us (597 TFLOP/s)
+// 13440 queries and keys, 16 heads of 64 in bfloat16 with the distance bias 1746 us,
+// 424 TFLOP/s; 4096 by 4096 of them 190 us with it and 115 us (597 TFLOP/s)
 // without; 2 x 4096, 16 / 4 heads of 128 308 us (893 TFLOP/s); 216 windows of 343
-// tokens, 8 heads of 32 in float16 263 us (347 us with pairs of one tile among the
+// tokens, 8 heads of 32 in float16 266 us (347 us with pairs of one tile among the
 // others: with an even number of CTAs half of them got all of the longer items).
 #include <atomic>
 

@@ -9,8 +9,7 @@
 // its two gradients 76 us each, 1480 TFLOP/s (53 x 4 tiles of 256 x 256 on 76 pairs
 // of CTAs: the third wave is 79 % full); of 1024 to 4096 with bias and GELU 102 us,
 // 1105 TFLOP/s (83 us without the activation: the epilogue's arithmetic, not the
-// tensor cores, which are active 56 % of the time); one token of 1024 to 4096 with
-// split sums 13 + 9 us, launches included.
+// tensor cores, which are active 56 % of the time); one token of 1024 to 4096 9.6 us.
 #include <atomic>
 
 #include "ffdp_tc.cuh"
